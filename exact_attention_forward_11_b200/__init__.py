@@ -1,10 +1,10 @@
 """B200 (sm_100a) fused attention forward: Python binding of the C ABI.
 
-The entry points below have the names and arguments of include/attn_b200.h and
+The entry points below have the names and arguments of the headers in include/ and
 only marshal arguments: every step of the computation runs in the CUDA kernels
 of libattn_b200.so. There is no CPU fallback; if the library is missing the
 calls raise. `forward`, `forward_from_host`, `quantize_fp8`, `forward_fp8`, `quantize_mxfp8`, `forward_mxfp8`,
-`backward` and `w4a16_matmul` are torch conveniences
+`backward`, `w4a16_matmul`, `kv4_append`, `kv4_read` and `forward_kv4` are torch conveniences
 that allocate outputs with torch (PyTorch serves only for device memory and
 streams) and call the same entry points.
 """
@@ -22,7 +22,7 @@ LIB_PATH = DEBUG_LIB_PATH if os.environ.get("ATTN_B200_DEBUG", "0") not in ("", 
 
 (ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_MISALIGNED, ATTN_ERR_CUDA, ATTN_ERR_TIMEOUT,
  ATTN_ERR_BOUNDS) = range(7)
-ATTN_BF16 = 0
+ATTN_BF16, ATTN_FP16 = 0, 1
 TILE = 128
 
 _lib = None
@@ -49,6 +49,10 @@ SIGNATURES = {
     "attn_fwd_debug_row_limit": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, ctypes.c_longlong, _P]),
     "attn_debug_build": (_I, []),
     "attn_debug_last_failure": (_I, [ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_longlong), _P]),
+    "attn_kv4_append": (_I, [_P] * 9 + [_I] * 10 + [_P]),
+    "attn_kv4_read": (_I, [_P] * 9 + [_I] * 10 + [_P]),
+    "attn_fwd_kv4": (_I, [_P] * 11 + [ctypes.c_size_t] + [_I] * 10 + [_F, _I, _I, _P]),
+    "attn_fwd_kv4_workspace_bytes": (ctypes.c_size_t, [_I] * 7),
     "attn_status_string": (ctypes.c_char_p, [_I]),
     "attn_abi_version": (_I, []),
 }
@@ -164,6 +168,29 @@ def attn_debug_last_failure(stream):
     if st != ATTN_OK:
         raise AttnError(st, "attn_debug_last_failure")
     return site.value, index.value
+
+
+def attn_kv4_append(k, v, k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, new_lens, B, Hkv, N, d, num_pages,
+                    page_size, max_pages, k_exp, v_exp, dtype, stream):
+    return load().attn_kv4_append(k, v, k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, new_lens, B, Hkv, N, d,
+                                  num_pages, page_size, max_pages, k_exp, v_exp, dtype, stream)
+
+
+def attn_kv4_read(k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, starts, k, v, B, Hkv, N, d, num_pages,
+                  page_size, max_pages, k_exp, v_exp, dtype, stream):
+    return load().attn_kv4_read(k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, starts, k, v, B, Hkv, N, d,
+                                num_pages, page_size, max_pages, k_exp, v_exp, dtype, stream)
+
+
+def attn_fwd_kv4(q, k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, q_lens, o, lse, workspace, workspace_bytes,
+                 B, Hq, Hkv, N, d, num_pages, page_size, max_pages, k_exp, v_exp, scale, causal, dtype, stream):
+    return load().attn_fwd_kv4(q, k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, q_lens, o, lse, workspace,
+                               workspace_bytes, B, Hq, Hkv, N, d, num_pages, page_size, max_pages, k_exp, v_exp,
+                               scale, causal, dtype, stream)
+
+
+def attn_fwd_kv4_workspace_bytes(B, Hq, Hkv, N, d, page_size, max_pages):
+    return load().attn_fwd_kv4_workspace_bytes(B, Hq, Hkv, N, d, page_size, max_pages)
 
 
 def use_library(path):
@@ -528,6 +555,180 @@ def w4a16_matmul(x, qweight, scales, zeros, out=None, stream=None, check=False, 
                              M, N, K, sp), "w4a16_gemm_splitk")
     _check_device(check, sp, "w4a16_gemm_splitk")
     return out
+
+
+class KV4Cache:
+    """The tensors of a 4-bit key/value cache (format: include/kv4_b200.h) and their
+    exponents: k_codes, v_codes uint8 [num_pages, Hkv, page_size, d / 2], k_sf, v_sf uint8
+    [num_pages, Hkv, page_size, d / 16]. The handle checks them once and keeps them;
+    KV4Cache.allocate makes new ones. A value reads back as code * scale * 2^exp:
+    exponents other than 0 suit tensors whose values are mostly below about 0.1 or
+    above 2000."""
+
+    __slots__ = ("k_codes", "k_sf", "v_codes", "v_sf", "k_exp", "v_exp", "num_pages", "heads", "page_size", "d",
+                 "device", "_ptrs")
+
+    def __init__(self, k_codes, k_sf, v_codes, v_sf, k_exp=0, v_exp=0):
+        import torch
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [num_pages, Hkv, page_size, d / 2]")
+        P, H, S, half = k_codes.shape
+        if half not in (32, 64) or S < 1 or S & (S - 1):
+            raise ValueError("d must be 64 or 128 and page_size a power of two")
+        for name, t, width in (("k_codes", k_codes, half), ("v_codes", v_codes, half), ("k_sf", k_sf, half // 8),
+                               ("v_sf", v_sf, half // 8)):
+            _expect(t, name, (P, H, S, width), torch.uint8, k_codes.device)
+        self.k_codes, self.k_sf, self.v_codes, self.v_sf = k_codes, k_sf, v_codes, v_sf
+        self.k_exp, self.v_exp = int(k_exp), int(v_exp)
+        self.num_pages, self.heads, self.page_size, self.d, self.device = P, H, S, 2 * half, k_codes.device
+        self._ptrs = tuple(t.data_ptr() for t in (k_codes, k_sf, v_codes, v_sf))
+
+    @classmethod
+    def allocate(cls, num_pages, heads, page_size, d, k_exp=0, v_exp=0, device="cuda"):
+        """A cache of num_pages empty pages (their slots hold nothing until written)."""
+        import torch
+        shape = (num_pages, heads, page_size)
+        new = [torch.empty((*shape, w), dtype=torch.uint8, device=device) for w in (d // 2, d // 16, d // 2, d // 16)]
+        return cls(*new, k_exp=k_exp, v_exp=v_exp)
+
+
+def _kv4_int32(t, name, shape, device):
+    import torch
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _kv4_rows(t, name, cache, heads=None):
+    """Sizes and element type of a 16-bit [B, H, N, d] argument of the cache calls."""
+    import torch
+    if t.dim() != 4 or not t.is_contiguous() or t.device != cache.device or \
+            (t.dtype is not torch.bfloat16 and t.dtype is not torch.float16):
+        raise ValueError(f"{name} must be a contiguous bf16 or fp16 tensor [B, H, N, d] on {cache.device}")
+    B, H, N, d = t.shape
+    if d != cache.d or (heads is not None and H != heads):
+        raise ValueError(f"{name} has {H} heads of width {d}: the cache has {cache.heads} of {cache.d}")
+    return B, H, N, ATTN_BF16 if t.dtype is torch.bfloat16 else ATTN_FP16
+
+
+def _kv4_tables(cache, block_table, seq_lens, B):
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be int32 [{B}, max_pages]")
+    return _kv4_int32(block_table, "block_table", block_table.shape, cache.device), \
+        _kv4_int32(seq_lens, "seq_lens", (B,), cache.device)
+
+
+class _kv4_place:
+    """Runs a launch with the tensors' device current and, for torch allocations, the
+    launch's stream current (a buffer made here then belongs to that stream)."""
+
+    __slots__ = ("device", "stream", "ctx")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.ctx = device, stream, []
+
+    def __enter__(self):
+        import torch
+        if self.device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(self.device))
+            self.ctx[-1].__enter__()
+        if self.stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        self.ctx.append(torch.cuda.stream(self.stream))
+        self.ctx[-1].__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        while self.ctx:
+            self.ctx.pop().__exit__(*exc)
+
+
+def kv4_append(cache, k, v, block_table, seq_lens, new_lens=None, stream=None, check=False):
+    """Quantises new tokens k, v (bf16 or fp16 [B, Hkv, N, d]) into the cache.
+
+    seq_lens (int32 [B]) are the lengths AFTER the call: token i < new_lens[b] (None: N
+    of each) goes to position seq_lens[b] - new_lens[b] + i, whose page is
+    block_table[b, position // page_size]. Asynchronous; a page number or length outside
+    the cache skips the write and is reported by attn_get_device_status()
+    (check=True waits and raises). Returns the cache."""
+    B, _, N, dt = _kv4_rows(k, "k", cache, cache.heads)
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device or not v.is_contiguous():
+        raise ValueError("v must be a contiguous tensor like k")
+    bt, sl = _kv4_tables(cache, block_table, seq_lens, B)
+    nl = None if new_lens is None else _kv4_int32(new_lens, "new_lens", (B,), cache.device)
+    with _kv4_place(cache.device, stream) as sp:
+        _check(attn_kv4_append(k.data_ptr(), v.data_ptr(), *cache._ptrs, bt, sl, nl, B, cache.heads, N, cache.d,
+                               cache.num_pages, cache.page_size, block_table.shape[1], cache.k_exp, cache.v_exp, dt,
+                               sp), "attn_kv4_append")
+        _check_device(check, sp, "attn_kv4_append")
+    return cache
+
+
+def kv4_read(cache, block_table, seq_lens, N, starts=None, dtype=None, k=None, v=None, stream=None, check=False):
+    """K, V (bf16 or fp16 [B, Hkv, N, d]) read back from the cache: row i holds position
+    starts[b] + i (None: i); rows at or behind seq_lens[b] are zero. Asynchronous;
+    bad page numbers and lengths as in kv4_append."""
+    import torch
+    B = seq_lens.shape[0]
+    bt, sl = _kv4_tables(cache, block_table, seq_lens, B)
+    st = None if starts is None else _kv4_int32(starts, "starts", (B,), cache.device)
+    shape = (B, cache.heads, int(N), cache.d)
+    with _kv4_place(cache.device, stream) as sp:
+        if k is None:
+            k = torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=cache.device)
+        if v is None:
+            v = torch.empty(shape, dtype=k.dtype, device=cache.device)
+        dt = _kv4_rows(k, "k", cache, cache.heads)[3]
+        for name, t in (("k", k), ("v", v)):
+            _expect(t, name, shape, k.dtype if dtype is None else dtype, cache.device)
+        _check(attn_kv4_read(*cache._ptrs, bt, sl, st, k.data_ptr(), v.data_ptr(), B, cache.heads, int(N), cache.d,
+                             cache.num_pages, cache.page_size, block_table.shape[1], cache.k_exp, cache.v_exp, dt,
+                             sp), "attn_kv4_read")
+        _check_device(check, sp, "attn_kv4_read")
+    return k, v
+
+
+def forward_kv4(q, cache, block_table, seq_lens, q_lens=None, causal=False, scale=None, out=None, lse=None,
+                with_lse=True, workspace=None, stream=None, check=False):
+    """O, LSE = attention of q (bf16 or fp16 [B, Hq, N, d]) over the 4-bit cache.
+
+    Hq is a multiple of the cache's heads (query head h reads cache head
+    h // (Hq / Hkv)). Query i < q_lens[b] (None: N of each) is the token at position
+    seq_lens[b] - q_lens[b] + i (append its key and value first, with the same
+    seq_lens); it sees every cached position, with causal=True only those up to its
+    own. N = 1 is a decoding step. Rows behind q_lens[b] are left as they were in out
+    and lse (zero where those are allocated here); a row that sees no key gets O = 0,
+    LSE = -inf. The workspace is allocated with torch unless given (see
+    attn_fwd_kv4_workspace_bytes). Asynchronous like forward(); bad page numbers and
+    lengths as in kv4_append."""
+    import torch
+    B, Hq, N, dt = _kv4_rows(q, "q", cache)
+    bt, sl = _kv4_tables(cache, block_table, seq_lens, B)
+    ql = None if q_lens is None else _kv4_int32(q_lens, "q_lens", (B,), cache.device)
+    with _kv4_place(cache.device, stream) as sp:
+        new = torch.empty if q_lens is None else torch.zeros
+        if out is None:
+            out = new(q.shape, dtype=q.dtype, device=q.device)
+        _expect(out, "out", q.shape, q.dtype, q.device)
+        if lse is None and with_lse:
+            lse = new((B, Hq, N), dtype=torch.float32, device=q.device)
+        if lse is not None:
+            _expect(lse, "lse", (B, Hq, N), torch.float32, q.device)
+        max_pages = block_table.shape[1]
+        need = attn_fwd_kv4_workspace_bytes(B, Hq, cache.heads, N, cache.d, cache.page_size, max_pages)
+        if workspace is None:
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        elif workspace.device != q.device or not workspace.is_contiguous() or \
+                workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {q.device}")
+        _check(attn_fwd_kv4(q.data_ptr(), *cache._ptrs, bt, sl, ql, out.data_ptr(), _ptr(lse), _ptr(workspace),
+                            0 if workspace is None else workspace.numel() * workspace.element_size(), B, Hq,
+                            cache.heads, N, cache.d, cache.num_pages, cache.page_size, max_pages, cache.k_exp,
+                            cache.v_exp, 0.0 if scale is None else float(scale), int(bool(causal)), dt, sp),
+               "attn_fwd_kv4")
+        _check_device(check, sp, "attn_fwd_kv4")
+    return out, lse
 
 
 def flops(B, H, N, d, causal):

@@ -1,4 +1,5 @@
-// attn_api.cu - host side of the C ABI declared in include/attn_b200.h.
+// attn_api.cu - host side of the C ABI declared in include/attn_b200.h and its
+// siblings (the 4-bit cache calls of include/kv4_b200.h are in kv4_api.cuh).
 //
 // Validates arguments (before anything touches the GPU), encodes TMA tensor maps
 // for the [B*H, N, d] operands, and launches the kernels on the caller's stream.
@@ -13,11 +14,14 @@
 
 #include "attn_b200.h"
 #include "attn_b200_testing.h"
+#include "kv4_b200.h"
 #include "w4a16_b200.h"
 #include "attn_bwd_kernel.cuh"
 #include "attn_fwd1_kernel.cuh"
 #include "attn_fwd_kernel.cuh"
 #include "fp8_prep_kernel.cuh"
+#include "kv4_attn_kernel.cuh"
+#include "kv4_cache_kernel.cuh"
 #include "mxfp8_quant_kernel.cuh"
 #include "w4a16_kernel.cuh"
 
@@ -738,3 +742,5 @@ attn_status attn_get_device_status(void* stream) {
 }
 
 }  // extern "C"
+
+#include "kv4_api.cuh"

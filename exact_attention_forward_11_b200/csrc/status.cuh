@@ -9,7 +9,8 @@
 // kStatusBounds into g_status, records its site and index (the first failure
 // since the last read wins) and returns false, and the caller skips the access.
 // Nothing traps. Without ATTN_DEBUG dbg_ok is the constant true and the checks
-// compile away.
+// compile away. (The 4-bit cache kernels check the device arrays of their callers
+// in every build and record kStatusBounds, see kv4_record.)
 #pragma once
 
 #include <cstdint>
@@ -40,6 +41,7 @@ enum DebugSite : uint32_t {
   kSiteTmaCoord = 10,      // TMA coordinate (x not a multiple of 16 elements, a negative store
                            // coordinate, or a unit outside the launch)
   kSiteW4Split = 11,       // partial slot or ticket index, split-K W4A16 GEMM
+  kSiteKv4Index = 12,      // page number, length or start outside the 4-bit cache (checked in release builds too)
 };
 
 __device__ uint32_t g_status;

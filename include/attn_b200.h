@@ -58,12 +58,14 @@ typedef enum {
   ATTN_ERR_MISALIGNED = 3,   /* a pointer is not 16-byte aligned                 */
   ATTN_ERR_CUDA = 4,         /* a CUDA runtime / driver call failed              */
   ATTN_ERR_TIMEOUT = 5,      /* a device pipeline wait ran out (see below)       */
-  ATTN_ERR_BOUNDS = 6        /* debug builds: a device-side index check failed   */
+  ATTN_ERR_BOUNDS = 6        /* a device-side index check failed: debug builds, and
+                                the 4-bit cache calls (kv4_b200.h) in every build */
 } attn_status;
 
-/* Element type of attn_fwd's q, k, v and o (passed as an int-sized enum). */
+/* Element type of a call's 16-bit tensors (passed as an int-sized enum). */
 typedef enum {
-  ATTN_BF16 = 0              /* bf16 inputs and output, fp32 accumulation        */
+  ATTN_BF16 = 0,             /* bf16 inputs and output, fp32 accumulation        */
+  ATTN_FP16 = 1              /* fp16: the 4-bit cache calls only (kv4_b200.h)    */
 } attn_dtype;
 
 /*
@@ -232,9 +234,9 @@ ATTN_API attn_status attn_bwd_noalloc(const void* q, const void* k, const void* 
 
 /*
  * attn_get_device_status - synchronises `stream`, then reads and clears the
- * device status word that kernels set when a pipeline wait timed out (or, in
- * a debug build, when an index check failed).
- * Returns ATTN_OK, ATTN_ERR_BOUNDS (debug builds: some check failed since the
+ * device status word that kernels set when a pipeline wait timed out (or when
+ * an index check failed: debug builds, and the 4-bit cache calls in every build).
+ * Returns ATTN_OK, ATTN_ERR_BOUNDS (some check failed since the
  * last read; it takes precedence over a timeout recorded in the same word),
  * ATTN_ERR_TIMEOUT, or ATTN_ERR_CUDA if the read failed.
  */
@@ -262,7 +264,8 @@ ATTN_API attn_status attn_get_device_status(void* stream);
  * forward), 3 MXFP8 scale-byte row load, 4 dK / dV row, 5 LSE / D_i load (dK dV
  * kernel), 6 dQ row and its LSE / D_i load, 7 FP8 tile scale, 8 MXFP8 block,
  * 9 W4A16 output column, 10 TMA coordinate or work unit, 11 split-K W4A16
- * partial slot (index: the slot). `site` and `index`
+ * partial slot (index: the slot), 12 page number, length or start outside the
+ * 4-bit cache. `site` and `index`
  * are host pointers. Returns ATTN_OK, ATTN_ERR_INVALID_ARG for a null pointer,
  * or ATTN_ERR_CUDA. In a release build the site is always 0.
  */
