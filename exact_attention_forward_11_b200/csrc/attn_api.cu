@@ -148,11 +148,12 @@ int sm_count() {
 // belongs to the function on the current device; later calls skip the driver
 // call). `tag` identifies the kernel. A failed launch forgets the flag, so a
 // context that was reset gets the attribute again on the next call.
-std::atomic<uint32_t> g_smem_done[64][16];
+constexpr int kSmemTags = 32;
+std::atomic<uint32_t> g_smem_done[64][kSmemTags];
 
 void forget_smem(int tag) {
   int dev = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && tag < 16)
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && tag < kSmemTags)
     g_smem_done[dev][tag].store(0u, std::memory_order_release);
 }
 
@@ -160,9 +161,9 @@ bool set_smem_once(const void* func, int bytes, int tag) {
   auto& done = g_smem_done;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return false;
-  if (dev < 64 && tag < 16 && done[dev][tag].load(std::memory_order_acquire)) return true;
+  if (dev < 64 && tag < kSmemTags && done[dev][tag].load(std::memory_order_acquire)) return true;
   if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-  if (dev < 64 && tag < 16) done[dev][tag].store(1u, std::memory_order_release);
+  if (dev < 64 && tag < kSmemTags) done[dev][tag].store(1u, std::memory_order_release);
   return true;
 }
 

@@ -56,6 +56,60 @@ dim3 kv4_move_grid(long long blocks, int sms) {
   return dim3(static_cast<unsigned>(need < cap ? need : cap), 2);
 }
 
+// How attn_fwd_kv4 runs a shape: rows per block, CTAs and workspace (host only; it
+// assumes the SMs of a B200, so that the size does not depend on the current device).
+struct Kv4Plan {
+  int nt, row_blocks, ctas;
+  size_t ml_bytes, workspace;
+};
+constexpr int kKv4Sms = 148;
+
+Kv4Plan kv4_plan(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {
+  Kv4Plan r;
+  const long long rows = static_cast<long long>(Hq / Hkv) * N;
+  r.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
+  r.row_blocks = static_cast<int>((rows + 8 * r.nt - 1) / (8 * r.nt));
+  const long long tiles = (static_cast<long long>(max_pages) * page_size + attn::kDecTile - 1) / attn::kDecTile;
+  const long long most = kKv4Sms * (r.nt == 1 ? 2 : 1);
+  const double units = static_cast<double>(tiles) * B * Hkv * r.row_blocks;
+  r.ctas = static_cast<int>(units < most ? units : most);
+  r.ml_bytes = static_cast<size_t>(2) * r.ctas * 8 * r.nt * sizeof(float2);
+  r.workspace = r.ml_bytes + static_cast<size_t>(2) * r.ctas * 8 * r.nt * d * sizeof(float);
+  return r;
+}
+
+template <class C, bool F16>
+attn_status launch_kv4_dec(const attn::Kv4AttnParams& p, int tag, cudaStream_t stream) {
+  auto kern = attn::kv4_decode_sm100<C, F16>;
+  if (!set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, tag)) return ATTN_ERR_CUDA;
+  kern<<<p.ctas, attn::kDecWarps * 32, C::SMEM_BYTES, stream>>>(p);
+  // the join may start (and read lengths) while the main kernel runs; it waits for it before
+  // it reads the workspace
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.c.B * p.Hq * p.N));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn::kv4_combine_sm100<C, F16>, p);
+  if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) {
+    forget_smem(tag);
+    return ATTN_ERR_CUDA;
+  }
+  return ATTN_OK;
+}
+
+template <int D, bool F16>
+attn_status launch_kv4_rows(const attn::Kv4AttnParams& p, const Kv4Plan& plan, cudaStream_t stream) {
+  const int tag = 16 + (D == 128 ? 0 : 6) + (F16 ? 3 : 0);
+  if (plan.nt == 1) return launch_kv4_dec<attn::Kv4DecCfg<D, 1>, F16>(p, tag, stream);
+  if (plan.nt == 2) return launch_kv4_dec<attn::Kv4DecCfg<D, 2>, F16>(p, tag + 1, stream);
+  return launch_kv4_dec<attn::Kv4DecCfg<D, 4>, F16>(p, tag + 2, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -113,8 +167,9 @@ attn_status attn_kv4_read(const void* k_codes, const void* k_sf, const void* v_c
 }
 
 size_t attn_fwd_kv4_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {
-  (void)B, (void)Hq, (void)Hkv, (void)N, (void)d, (void)page_size, (void)max_pages;
-  return 0;
+  if (B < 1 || Hq < 1 || Hkv < 1 || N < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
+  if (page_size < 1 || page_size > 65536 || (page_size & (page_size - 1)) != 0 || max_pages < 1) return 0;
+  return kv4_plan(B, Hq, Hkv, N, d, page_size, max_pages).workspace;
 }
 
 attn_status attn_fwd_kv4(const void* q, const void* k_codes, const void* k_sf, const void* v_codes, const void* v_sf,
@@ -146,11 +201,14 @@ attn_status attn_fwd_kv4(const void* q, const void* k_codes, const void* k_sf, c
   p.N = N;
   p.causal = causal;
   p.scale_log2 = std::ldexp(scale * 1.4426950408889634f, k_exp);
-  auto kern = d == 128
-                  ? (dtype == ATTN_FP16 ? attn::kv4_attn_row_sm100<128, true> : attn::kv4_attn_row_sm100<128, false>)
-                  : (dtype == ATTN_FP16 ? attn::kv4_attn_row_sm100<64, true> : attn::kv4_attn_row_sm100<64, false>);
-  kern<<<static_cast<unsigned>(static_cast<long long>(B) * Hq * N), 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  const Kv4Plan plan = kv4_plan(B, Hq, Hkv, N, d, page_size, max_pages);
+  p.row_blocks = plan.row_blocks;
+  p.ctas = plan.ctas;
+  p.part_ml = static_cast<float2*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.ml_bytes);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d == 128) return dtype == ATTN_FP16 ? launch_kv4_rows<128, true>(p, plan, st) : launch_kv4_rows<128, false>(p, plan, st);
+  return dtype == ATTN_FP16 ? launch_kv4_rows<64, true>(p, plan, st) : launch_kv4_rows<64, false>(p, plan, st);
 }
 
 }  // extern "C"

@@ -1,13 +1,62 @@
-// kv4_attn_kernel.cuh - attention over the 4-bit cache (include/kv4_b200.h).
+// kv4_attn_kernel.cuh - attention over the 4-bit cache for few query rows per cached head
+// (include/kv4_b200.h): decoding steps, where the cache's bytes are all that counts.
 //
-// One CTA of 128 threads per query row, two passes over each tile of 128 keys: a thread
-// scores one key (fp32), then a thread owns one output channel and sums the tile's
-// P V. Online softmax over the tiles.
+// For one (sequence b, cached head h) the G = Hq / Hkv query heads times N query tokens are
+// R = G N rows that see the same keys; they are taken in blocks of 8 NT rows. With K^ and V^ the
+// values the codes stand for, the kernel computes S^T = K^ Q^T and O^T = V^^T P^T (keys, and then
+// channels, on the 16-wide M side of mma.m16n8k16, the rows on the 8-wide N side), so that no
+// tensor-core work is spent on rows that do not exist and the accumulators of a row are scalars
+// of a lane: with g = lane / 4, t = lane % 4, a lane holds rows 2 t, 2 t + 1 of every row tile.
+//  * A lane takes the codes it needs as whole vectors: of key g the D / 4 consecutive channels
+//    [D/4 t, D/4 (t+1)) for S (the order of channels in a dot product is free, and q is loaded in the
+//    same order), and for P V of four keys the D / 8 channels [D/8 g, D/8 (g+1)) (the order of rows in
+//    O^T is free too).
+//  * E2M1 codes become f16 pairs with one conversion per byte and one multiplication by the block
+//    scale, both exact. For V the nibbles of two keys are first interleaved (a shift and a bit
+//    select per four pairs), since P V pairs values along the keys.
+//  * P leaves S^T with the keys along lanes' groups and is needed with the keys along t: one
+//    movmatrix per 8 keys x 8 rows.
+// Every warp streams its own 32 keys of each 256-key tile through a ring of cp.async stages
+// and keeps its own running maximum, sum and O; warps meet only where a segment ends. The
+// maximum moves only when a score exceeds it by more than 8 (log2 units), so most steps cost
+// one vote and no reduction across lanes; P <= 2^8 then, well inside f16.
+//
+// Schedule: the 256-key tiles of all (b, h, row block) make one long list that is cut into
+// equal runs, one per CTA, so uneven lengths balance without the host knowing them. A run
+// that covers part of a (b, h, row block) writes its unnormalised O, maximum and sum to the
+// workspace (two slots per CTA: a run's first and last item); kv4_combine_sm100 joins
+// them in the order of the CTAs, so results do not depend on timing.
+//
+// Bound: HBM at 4.5 bits a value is 13e12 values / s; a value costs about half a conversion
+// and half a multiplication (64 lanes / clk / SM each).
 #pragma once
 
 #include "kv4_cache_kernel.cuh"
 
 namespace attn {
+
+constexpr int kDecWarps = 8;
+constexpr int kDecKeys = 32;                       // keys of a warp's step
+constexpr int kDecTile = kDecWarps * kDecKeys;     // 256
+
+template <int D_, int NT_>
+struct Kv4DecCfg {
+  static constexpr int D = D_, NT = NT_, ROWS = 8 * NT;
+  static constexpr int CODE_ROW = D / 2, SF_ROW = D / 16;
+  static constexpr int CTAS_PER_SM = NT == 1 ? 2 : 1;
+  static constexpr int STAGES = (NT == 1 ? 3 : 6) * (D == 64 ? 2 : 1);
+  // a stage of one warp: key codes, value codes, key scales, value scales
+  static constexpr int ST_VC = kDecKeys * CODE_ROW, ST_KS = 2 * kDecKeys * CODE_ROW,
+                       ST_VS = ST_KS + kDecKeys * SF_ROW, STAGE = ST_VS + kDecKeys * SF_ROW;
+  static constexpr int RING = kDecWarps * STAGES * STAGE;
+  static constexpr int O_LD = D + 8;               // floats between rows of a warp's O in the merge buffer
+  static constexpr int MERGE = kDecWarps * ROWS * O_LD * 4;
+  static constexpr int SMEM_ML = RING > MERGE ? RING : MERGE;            // [warps][ROWS] (max, sum)
+  static constexpr bool QREG = NT <= 2;            // q fragments in registers, else in shared memory
+  static constexpr int KSTEPS = D / 16;
+  static constexpr int SMEM_Q = SMEM_ML + kDecWarps * ROWS * 8;
+  static constexpr int SMEM_BYTES = SMEM_Q + (QREG ? 0 : KSTEPS * NT * 32 * 8);
+};
 
 struct Kv4AttnParams {
   Kv4Cache c;
@@ -15,89 +64,536 @@ struct Kv4AttnParams {
   uint8_t* o;
   float* lse;                // or nullptr
   const int* q_lens;         // or nullptr
+  float* part_o;             // workspace: [2 ctas][ROWS][D]
+  float2* part_ml;           // [2 ctas][ROWS] (maximum in log2 units, sum)
   int Hq, N, causal;
+  int row_blocks;            // ceil(Hq / Hkv * N / ROWS)
+  int ctas;                  // CTAs of the main kernel (at most; see kv4_runs)
   float scale_log2;          // scale * log2(e) * 2^k_exp
 };
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(128) kv4_attn_row_sm100(const Kv4AttnParams p) {
-  __shared__ float qs[D], ps[128], red[4];
-  __shared__ uint32_t rows[128];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int i = blockIdx.x % p.N, hq = (blockIdx.x / p.N) % p.Hq, b = blockIdx.x / p.N / p.Hq;
-  const int h = hq / (p.Hq / p.c.H);
-  const int n = p.q_lens != nullptr ? kv4_clamp(p.q_lens[b], p.N) : p.N;
-  if (i >= n) return;
-  const int len = kv4_len(p.c, b);
-  const int end = p.causal ? min(len, len - n + i + 1) : len;
-  const size_t r = blockIdx.x;
-  if (tid < D / 2) {
-    const float2 f = f32x2_from_16<F16>(reinterpret_cast<const uint32_t*>(p.q + r * D * 2)[tid]);
-    qs[2 * tid] = f.x;
-    qs[2 * tid + 1] = f.y;
+__device__ __forceinline__ int kv4_qlen(const Kv4AttnParams& p, int b) {
+  return p.q_lens != nullptr ? kv4_clamp(p.q_lens[b], p.N) : p.N;
+}
+// Tiles of one (head, row block) of sequence b.
+__device__ __forceinline__ int kv4_tiles(const Kv4AttnParams& p, int b) {
+  return kv4_qlen(p, b) == 0 ? 0 : (kv4_len(p.c, b) + kDecTile - 1) / kDecTile;
+}
+
+// The cut of `units` tiles into runs: CTA c of n = min(ctas, units) takes [start(c), start(c + 1)).
+struct Kv4Runs {
+  long long units;
+  int n;
+  __device__ __forceinline__ Kv4Runs(long long u, int ctas) : units(u), n(static_cast<int>(u < ctas ? u : ctas)) {}
+  __device__ __forceinline__ long long start(int c) const { return units * c / n; }
+  __device__ __forceinline__ int cta_of(long long u) const { return static_cast<int>(((u + 1) * n - 1) / units); }
+};
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  return v;
+}
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(valid ? BYTES : 0), "n"(BYTES)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// whether one of the four scale bytes is a NaN
+__device__ __forceinline__ bool any_nan_scale(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u; }
+
+// A query row's exponent: q 2^-e lies below 2^10 in magnitude and its largest value at or above 2^9
+// (rows of zeros and of very small values: as far as an fp32 power of two goes; a row with an
+// infinity or NaN is left as it is). Returns the exponent field of 2^e.
+__device__ __forceinline__ int kv4_row_exp(float amax) {
+  const int ef = static_cast<int>(__float_as_uint(amax) >> 23);
+  return ef == 255 ? 127 : max(ef, 10) - 9;
+}
+
+template <class C, bool F16>
+__global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm100(const Kv4AttnParams p) {
+  constexpr int D = C::D, NT = C::NT, ROWS = C::ROWS;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t smem0 = b200::smem_addr(smem_raw);
+  const uint32_t ring = smem0 + warp * C::STAGES * C::STAGE;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  // this CTA's run, and the (sequence, tiles before it) where it starts
+  const int per_b = p.c.H * p.row_blocks;
+  long long total = 0;
+  for (int b = lane; b < p.c.B; b += 32) total += kv4_tiles(p, b);
+  const Kv4Runs runs(warp_sum(total) * per_b, p.ctas);
+  if (static_cast<int>(blockIdx.x) >= runs.n) return;
+  long long u = runs.start(blockIdx.x);
+  const long long u_end = runs.start(blockIdx.x + 1);
+  int b = 0;
+  long long b_first = 0;                            // first unit of sequence b
+  for (int b0 = 0;; b0 += 32) {
+    const long long mine = b0 + lane < p.c.B ? static_cast<long long>(kv4_tiles(p, b0 + lane)) * per_b : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, s);
+      if (lane >= s) incl += o;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, b_first + incl > u);
+    if (hit != 0u) {
+      const int l = __ffs(hit) - 1;
+      b = b0 + l;
+      b_first += __shfl_sync(0xffffffffu, incl - mine, l);
+      break;
+    }
+    b_first += __shfl_sync(0xffffffffu, incl, 31);
   }
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int j0 = 0; j0 < end; j0 += 128) {
-    __syncthreads();
-    const int j = j0 + tid;
-    float s = -INFINITY;
-    uint32_t row = 0xFFFFFFFFu;
-    if (j < end && kv4_row(p.c, p.c.block_table[static_cast<long long>(b) * p.c.max_pages + (j >> p.c.page_shift)], h, j, row)) {
-      s = 0.f;
-      for (int blk = 0; blk < D / 16; ++blk) {
-        const uint2 w = *reinterpret_cast<const uint2*>(p.c.codes[0] + static_cast<size_t>(row) * (D / 2) + blk * 8);
-        const uint32_t byte = p.c.sf[0][static_cast<size_t>(row) * (D / 16) + blk];
-        const uint32_t s2 = b200::f16x2_from_e4m3x2(static_cast<uint16_t>(byte | (byte << 8)));
-        uint32_t f[4], g[4];
-        f16x2_from_e2m1x8(w.x, f);
-        f16x2_from_e2m1x8(w.y, g);
-        for (int k = 0; k < 4; ++k) {
-          const float2 a = f32x2_from_f16x2(hmul2(f[k], s2)), c = f32x2_from_f16x2(hmul2(g[k], s2));
-          s += a.x * qs[blk * 16 + 2 * k] + a.y * qs[blk * 16 + 2 * k + 1] + c.x * qs[blk * 16 + 8 + 2 * k] +
-               c.y * qs[blk * 16 + 9 + 2 * k];
+  const long long u_begin = u;
+
+  while (u < u_end) {
+    int T = kv4_tiles(p, b);
+    while (u >= b_first + static_cast<long long>(T) * per_b) {   // sequences without tiles are passed over
+      b_first += static_cast<long long>(T) * per_b;
+      T = kv4_tiles(p, ++b);
+    }
+    const int item = static_cast<int>((u - b_first) / T);
+    const long long item_first = b_first + static_cast<long long>(item) * T;
+    const int h = item / p.row_blocks, rb = item % p.row_blocks;
+    const int t0 = static_cast<int>(u - item_first);
+    const int t1 = static_cast<int>(min(static_cast<long long>(T), u_end - item_first));
+    const int len = kv4_len(p.c, b), n = kv4_qlen(p, b);
+    const int R = p.Hq / p.c.H * p.N;
+    const size_t row0 = (static_cast<size_t>(b) * p.c.H + h) * R;      // rows of (b, h) are contiguous in q and o
+
+    // ---- q fragments: lane (g, t) takes channels [D/4 t, D/4 (t+1)) of row g of each tile
+    uint32_t qf[C::QREG ? NT : 1][C::KSTEPS][2];
+    float cs[NT][2], m[NT][2], l[NT][2];
+    int lim[NT][2];                                 // last visible key of rows 2 t, 2 t + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = rb * ROWS + nt * 8 + g;
+      uint32_t w[D / 8];
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 x = r < R ? reinterpret_cast<const uint4*>(p.q + ((row0 + r) * D + t * (D / 4)) * 2)[i]
+                              : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const float2 f = f32x2_from_16<F16>(w[i]);
+        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int e = kv4_row_exp(amax);
+      const float down = __int_as_float((254 - e) << 23), up = __int_as_float(e << 23);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const float2 f = f32x2_from_16<F16>(w[i]);
+        w[i] = b200::pack_f16x2(f.x * down, f.y * down);
+      }
+#pragma unroll
+      for (int k = 0; k < C::KSTEPS; ++k) {
+        if constexpr (C::QREG) {
+          qf[nt][k][0] = w[2 * k];
+          qf[nt][k][1] = w[2 * k + 1];
+        } else if (warp == nt % kDecWarps) {
+          *reinterpret_cast<uint2*>(smem_raw + C::SMEM_Q + ((k * NT + nt) * 32 + lane) * 8) =
+              make_uint2(w[2 * k], w[2 * k + 1]);
         }
       }
-      s *= p.scale_log2;
-    } else {
-      row = 0xFFFFFFFFu;
-    }
-    rows[tid] = row;
-    float mx = s;
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) red[warp] = mx;
-    __syncthreads();
-    const float m_new = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float m_use = m_new == -INFINITY ? 0.f : m_new;
-    const float pj = exp2f(s - m_use);
-    ps[tid] = pj;
-    float sum = pj;
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncthreads();
-    if (lane == 0) red[warp] = sum;
-    __syncthreads();
-    const float alpha = exp2f(m - m_use);
-    l = l * alpha + (red[0] + red[1] + red[2] + red[3]);
-    m = m_new;
-    acc *= alpha;
-    if (tid < D) {
-      const int kn = min(128, end - j0);
-      for (int k = 0; k < kn; ++k) {
-        const uint32_t rk = rows[k];
-        if (rk == 0xFFFFFFFFu) continue;
-        const uint32_t cb = reinterpret_cast<const uint32_t*>(p.c.codes[1] + static_cast<size_t>(rk) * (D / 2))[tid >> 3];
-        const uint32_t byte = p.c.sf[1][static_cast<size_t>(rk) * (D / 16) + (tid >> 4)];
-        uint32_t f[4];
-        f16x2_from_e2m1x8(cb, f);
-        const float2 a = f32x2_from_f16x2(hmul2(f[(tid >> 1) & 3], b200::f16x2_from_e4m3x2(static_cast<uint16_t>(byte | (byte << 8)))));
-        acc += ps[k] * ((tid & 1) ? a.y : a.x);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        cs[nt][j] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + j)) * p.scale_log2;
+        m[nt][j] = -INFINITY;
+        l[nt][j] = 0.f;
+        const int rr = rb * ROWS + nt * 8 + 2 * t + j;
+        lim[nt][j] = p.causal ? len - n + rr % p.N : len - 1;
       }
     }
+    if constexpr (!C::QREG) __syncthreads();
+    const int lim_all = p.causal ? len - n : len - 1;       // every row sees the keys up to here
+    float o[NT][D / 16][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
+
+    // ---- the warp's pipeline over its 32-key steps
+    const int* table = p.c.block_table + static_cast<long long>(b) * p.c.max_pages;
+    auto page_of = [&](int tt) {                    // page of this lane's key in tile tt
+      const int key = tt * kDecTile + warp * kDecKeys + lane;
+      return tt < t1 && key < len ? table[key >> p.c.page_shift] : 0;
+    };
+    auto issue = [&](int tt, int page) {
+      if (tt < t1) {
+        const uint32_t st = ring + static_cast<uint32_t>((tt - t0) % C::STAGES) * C::STAGE;
+        const int key = tt * kDecTile + warp * kDecKeys + lane;
+        uint32_t row = 0u;
+        const bool ok = key < len && kv4_row(p.c, page, h, key, row);
+        // keys sit in K's stage in the order of the S^T rows they become: 16-key group, then
+        // slot 2 (k % 4) + k / 4 (+ 8 for its upper half), see V's loads
+        const int k16 = lane & 15;
+        const int kslot = (lane & 16) + (k16 & 8) + 2 * (k16 & 3) + ((k16 >> 2) & 1);
+        cp_async_small<C::SF_ROW>(st + C::ST_KS + kslot * C::SF_ROW, p.c.sf[0] + static_cast<size_t>(ok ? row : 0u) * C::SF_ROW, ok);
+        cp_async_small<C::SF_ROW>(st + C::ST_VS + lane * C::SF_ROW, p.c.sf[1] + static_cast<size_t>(ok ? row : 0u) * C::SF_ROW, ok);
+        constexpr int CH = C::CODE_ROW / 16;
+        const int ch = lane % CH;
+        const uint32_t mark = ok ? row : 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int r = lane / CH + i * (32 / CH);
+          const uint32_t rr = __shfl_sync(0xffffffffu, mark, r);
+          const bool v = rr != 0xFFFFFFFFu;
+          const size_t off = static_cast<size_t>(v ? rr : 0u) * C::CODE_ROW + ch * 16;
+          const int r16 = r & 15;
+          const int slot = (r & 16) + (r16 & 8) + 2 * (r16 & 3) + ((r16 >> 2) & 1);
+          cp_async_16(st + slot * C::CODE_ROW + ch * 16, p.c.codes[0] + off, v);
+          const int vch = CH == 4 ? ch ^ (r & 2) : ch;       // (D = 128) spreads V's 8-byte loads over all banks
+          cp_async_16(st + C::ST_VC + r * C::CODE_ROW + vch * 16, p.c.codes[1] + off, v);
+        }
+      }
+      cp_async_commit();
+    };
+    int page = page_of(t0);
+#pragma unroll
+    for (int s = 0; s < C::STAGES - 1; ++s) {
+      const int nx = page_of(t0 + s + 1);
+      issue(t0 + s, page);
+      page = nx;
+    }
+    for (int tt = t0; tt < t1; ++tt) {
+      cp_async_wait<C::STAGES - 2>();
+      __syncwarp();
+      const int nx = page_of(tt + C::STAGES);
+      issue(tt + C::STAGES - 1, page);
+      page = nx;
+      const uint8_t* st = smem_raw + (ring - smem0) + static_cast<uint32_t>((tt - t0) % C::STAGES) * C::STAGE;
+      const int base = tt * kDecTile + warp * kDecKeys;
+      if (base >= len) continue;
+      // ---- S^T of 32 keys
+      float s[2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t kw[2][D / 32];                     // codes of keys (S^T rows) g and g + 8
+        uint32_t ks[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int slot = 16 * mt + 8 * j + g;
+          const uint8_t* a = st + slot * C::CODE_ROW + t * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(a);
+            kw[j][0] = x.x, kw[j][1] = x.y, kw[j][2] = x.z, kw[j][3] = x.w;
+            ks[j] = b200::f16x2_from_e4m3x2(*reinterpret_cast<const uint16_t*>(st + C::ST_KS + slot * 8 + 2 * t));
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(a);
+            kw[j][0] = x.x, kw[j][1] = x.y;
+            const uint32_t by = st[C::ST_KS + slot * 4 + t];
+            ks[j] = b200::f16x2_from_e4m3x2(static_cast<uint16_t>(by | (by << 8)));
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[mt][nt][j] = 0.f;
+#pragma unroll
+        for (int wd = 0; wd < D / 32; ++wd) {       // a word: 8 channels, two k-steps
+          uint32_t f[2][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            f16x2_from_e2m1x8(kw[j][wd], f[j]);
+            const uint32_t sc = D == 128 ? __byte_perm(ks[j], 0u, wd < 2 ? 0x1010 : 0x3232) : ks[j];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[j][i] = hmul2(f[j][i], sc);
+          }
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t a[4] = {f[0][2 * hf], f[1][2 * hf], f[0][2 * hf + 1], f[1][2 * hf + 1]};
+            const int k = 2 * wd + hf;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (C::QREG) {
+                mma_16816(s[mt][nt], a, qf[nt][k][0], qf[nt][k][1]);
+              } else {
+                const uint2 qq = *reinterpret_cast<const uint2*>(smem_raw + C::SMEM_Q + ((k * NT + nt) * 32 + lane) * 8);
+                mma_16816(s[mt][nt], a, qq.x, qq.y);
+              }
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[mt][nt][j] *= cs[nt][j & 1];
+      // ---- masks: only steps that some row does not see to their end
+      uint32_t vnan = 0u;                           // (masked steps) keys whose values hold a NaN
+      if (base + kDecKeys - 1 > lim_all) {
+        bool bad;
+        if constexpr (D == 128) {
+          const uint2 x = *reinterpret_cast<const uint2*>(st + C::ST_VS + lane * 8);
+          bad = any_nan_scale(x.x) || any_nan_scale(x.y);
+        } else {
+          bad = any_nan_scale(*reinterpret_cast<const uint32_t*>(st + C::ST_VS + lane * 4));
+        }
+        vnan = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = 16 * mt + 8 * (j >> 1) + (g >> 1) + 4 * (g & 1);   // the key of this S^T row
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              // a NaN value reaches the rows that see it through their scores, and no other
+              if ((vnan >> k) & 1u) s[mt][nt][j] = __int_as_float(0x7FC00000);
+              if (base + k > lim[nt][j & 1]) s[mt][nt][j] = -INFINITY;
+            }
+          }
+      }
+      // ---- online softmax
+      bool grow = false;
+      float mx[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          mx[nt][j] = fmaxf(fmaxf(s[0][nt][j], s[0][nt][j + 2]), fmaxf(s[1][nt][j], s[1][nt][j + 2]));
+          grow = grow || mx[nt][j] > m[nt][j] + 8.f;
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float x = mx[nt][j];
+#pragma unroll
+            for (int sft = 4; sft < 32; sft <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sft));
+            const float mn = fmaxf(m[nt][j], x);
+            const float al = mn == -INFINITY ? 1.f : b200::ex2_approx(m[nt][j] - mn);
+            m[nt][j] = mn;
+            l[nt][j] *= al;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[nt][i][j] *= al;
+              o[nt][i][j + 2] *= al;
+            }
+          }
+      }
+      uint32_t pb[2][NT][2];                        // P^T fragments: keys 2 t (+1), and + 8, of each 16-key tile
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float p0 = b200::ex2_approx(s[mt][nt][2 * hf] - m0), p1 = b200::ex2_approx(s[mt][nt][2 * hf + 1] - m1);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            pb[mt][nt][hf] = movmatrix(b200::pack_f16x2(p0, p1));
+          }
+      }
+      // ---- O^T += V^^T P^T: S^T rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 are keys t, t + 4, t + 8, t + 12
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t vw[4][D / 64];
+        uint32_t by[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 16 * mt + t + 4 * i;
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(st + C::ST_VC + r * 64 + (((g >> 1) ^ (r & 2)) << 4) + (g & 1) * 8);
+            vw[i][0] = x.x, vw[i][1] = x.y;
+            by[i] = st[C::ST_VS + r * 8 + g];
+          } else {
+            vw[i][0] = *reinterpret_cast<const uint32_t*>(st + C::ST_VC + r * 32 + g * 4);
+            by[i] = st[C::ST_VS + r * 4 + (g >> 1)];
+          }
+          if (vnan != 0u && (by[i] & 0x7Fu) == 0x7Fu) by[i] = 0u;
+        }
+        uint32_t vs[2];
+#pragma unroll
+        for (int pr = 0; pr < 2; ++pr)
+          vs[pr] = b200::f16x2_from_e4m3x2(static_cast<uint16_t>(by[2 * pr] | (by[2 * pr + 1] << 8)));
+#pragma unroll
+        for (int wd = 0; wd < D / 64; ++wd) {
+          uint32_t ev[2][4], od[2][4];              // f16 pairs (key, key + 4) of even and odd channels
+#pragma unroll
+          for (int pr = 0; pr < 2; ++pr) {
+            const uint32_t wa = vw[2 * pr][wd], wb = vw[2 * pr + 1][wd];
+            f16x2_from_e2m1x8((wa & 0x0F0F0F0Fu) | ((wb << 4) & 0xF0F0F0F0u), ev[pr]);
+            f16x2_from_e2m1x8(((wa >> 4) & 0x0F0F0F0Fu) | (wb & 0xF0F0F0F0u), od[pr]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              ev[pr][i] = hmul2(ev[pr][i], vs[pr]);
+              od[pr][i] = hmul2(od[pr][i], vs[pr]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a[4] = {ev[0][i], od[0][i], ev[1][i], od[1][i]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][4 * wd + i], a, pb[mt][nt][0], pb[mt][nt][1]);
+          }
+        }
+      }
+    }
+    cp_async_wait<0>();
+
+    // ---- the segment ends: the warps' results meet in shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int sft = 4; sft < 32; sft <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], sft);
+    __syncthreads();
+    float* mo = reinterpret_cast<float*>(smem_raw);
+    float2* ml = reinterpret_cast<float2*>(smem_raw + C::SMEM_ML);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = nt * 8 + 2 * t + j;
+        if (g == 0) ml[warp * ROWS + r] = make_float2(m[nt][j], l[nt][j]);
+        float* dst = mo + (warp * ROWS + r) * C::O_LD + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          *reinterpret_cast<float4*>(dst + 4 * i) =
+              make_float4(o[nt][2 * i][j], o[nt][2 * i][j + 2], o[nt][2 * i + 1][j], o[nt][2 * i + 1][j + 2]);
+      }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == T;
+    const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
+    constexpr int V4 = D / 4;                       // float4 per row
+    for (int i = tid; i < ROWS * V4; i += kDecWarps * 32) {
+      const int r = i / V4, d4 = i % V4;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ml[w * ROWS + r].x);
+      const float Mu = M == -INFINITY ? 0.f : M;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      float L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float2 x = ml[w * ROWS + r];
+        const float f = b200::ex2_approx(x.x - Mu);
+        const float4 v = *reinterpret_cast<const float4*>(mo + (w * ROWS + r) * C::O_LD + 4 * d4);
+        L += f * x.y;
+        a.x += f * v.x, a.y += f * v.y, a.z += f * v.z, a.w += f * v.w;
+      }
+      if (whole) {
+        const int rr = rb * ROWS + r;
+        if (rr < R && rr % p.N < n) {
+          const float inv = L == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / L;
+          reinterpret_cast<uint2*>(p.o)[(row0 + rr) * V4 + d4] =
+              make_uint2(pack_16<F16>(a.x * inv, a.y * inv), pack_16<F16>(a.z * inv, a.w * inv));
+          if (p.lse != nullptr && d4 == 0)
+            p.lse[row0 + rr] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+        }
+      } else {
+        reinterpret_cast<float4*>(p.part_o)[(static_cast<size_t>(slot) * ROWS + r) * V4 + d4] = a;
+        if (d4 == 0) p.part_ml[static_cast<size_t>(slot) * ROWS + r] = make_float2(M, L);
+      }
+    }
+    __syncthreads();
+    u = item_first + t1;
   }
-  if (tid < D) {
-    const float o = l > 0.f || l != l ? acc / l * f32_exp2i(p.c.exp[1]) : 0.f;
-    reinterpret_cast<uint16_t*>(p.o)[r * D + tid] = static_cast<uint16_t>(pack_16<F16>(o, 0.f));
+}
+
+// Joins the parts of the (b, h, row block) that several runs share, and writes the rows of
+// sequences without keys. One CTA of 128 threads per row: its four warps take every fourth
+// part, a lane 4 channels (D = 128; two lanes' worth idle at D = 64).
+template <class C, bool F16>
+__global__ void __launch_bounds__(128) kv4_combine_sm100(const Kv4AttnParams p) {
+  constexpr int D = C::D, ROWS = C::ROWS, V4 = D / 4;
+  __shared__ float4 so[4][V4];
+  __shared__ float2 sml[4];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int R = p.Hq / p.c.H * p.N;
+  const int rr = blockIdx.x % R, bh = blockIdx.x / R;
+  const int b = bh / p.c.H, h = bh % p.c.H, rb = rr / ROWS, r = rr % ROWS;
+  const int n = kv4_qlen(p, b);
+  const int per_b = p.c.H * p.row_blocks;
+  long long total = 0, before = 0;
+  for (int i = lane; i < p.c.B; i += 32) {
+    const int T = kv4_tiles(p, i);
+    total += T;
+    if (i < b) before += T;
   }
-  if (p.lse != nullptr && tid == 0) p.lse[r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  const Kv4Runs runs(warp_sum(total) * per_b, p.ctas);
+  const int T = kv4_tiles(p, b);
+  const size_t row = static_cast<size_t>(bh) * R + rr;
+  // every CTA waits, so that this grid ends after the main one whatever it has to do
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (rr % p.N >= n) return;
+  if (T == 0) {
+    if (warp == 0 && lane < V4) reinterpret_cast<uint2*>(p.o)[row * V4 + lane] = make_uint2(0u, 0u);
+    if (p.lse != nullptr && tid == 0) p.lse[row] = -INFINITY;
+    return;
+  }
+  const long long u0 = warp_sum(before) * per_b + static_cast<long long>(h * p.row_blocks + rb) * T;
+  const int c0 = runs.cta_of(u0), c1 = runs.cta_of(u0 + T - 1);
+  if (c0 == c1) return;
+  // part of CTA c: its first segment, except where it came to this item from another
+  auto slot_of = [&](int c) { return 2 * c + (c == c0 && runs.start(c0) < u0 ? 1 : 0); };
+  float M = -INFINITY, L = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0 + warp; c <= c1; c += 4) {
+    const size_t at = static_cast<size_t>(slot_of(c)) * ROWS + r;
+    const float2 x = __ldcg(p.part_ml + at);
+    const float4 v = lane < V4 ? __ldcg(reinterpret_cast<const float4*>(p.part_o) + at * V4 + lane) : a;
+    const float Mn = fmaxf(M, x.x);
+    const float Mu = Mn == -INFINITY ? 0.f : Mn;
+    const float fo = b200::ex2_approx(M - Mu), fn = b200::ex2_approx(x.x - Mu);
+    L = L * fo + x.y * fn;
+    a.x = a.x * fo + v.x * fn, a.y = a.y * fo + v.y * fn, a.z = a.z * fo + v.z * fn, a.w = a.w * fo + v.w * fn;
+    M = Mn;
+  }
+  if (lane < V4) so[warp][lane] = a;
+  if (lane == 0) sml[warp] = make_float2(M, L);
+  __syncthreads();
+  if (tid >= V4) return;
+  M = fmaxf(fmaxf(sml[0].x, sml[1].x), fmaxf(sml[2].x, sml[3].x));
+  const float Mu = M == -INFINITY ? 0.f : M;
+  L = 0.f;
+  a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = b200::ex2_approx(sml[w].x - Mu);
+    const float4 v = so[w][tid];
+    L += f * sml[w].y;
+    a.x += f * v.x, a.y += f * v.y, a.z += f * v.z, a.w += f * v.w;
+  }
+  const float inv = L == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / L;
+  reinterpret_cast<uint2*>(p.o)[row * V4 + tid] =
+      make_uint2(pack_16<F16>(a.x * inv, a.y * inv), pack_16<F16>(a.z * inv, a.w * inv));
+  if (p.lse != nullptr && tid == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
 }
 
 }  // namespace attn
