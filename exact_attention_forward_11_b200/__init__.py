@@ -573,8 +573,8 @@ class KV4Cache:
         if k_codes.dim() != 4:
             raise ValueError("k_codes must be [num_pages, Hkv, page_size, d / 2]")
         P, H, S, half = k_codes.shape
-        if half not in (32, 64) or S < 1 or S & (S - 1):
-            raise ValueError("d must be 64 or 128 and page_size a power of two")
+        if half not in (32, 64) or S < 16 or S & (S - 1):
+            raise ValueError("d must be 64 or 128 and page_size a power of two, 16 or more")
         for name, t, width in (("k_codes", k_codes, half), ("v_codes", v_codes, half), ("k_sf", k_sf, half // 8),
                                ("v_sf", v_sf, half // 8)):
             _expect(t, name, (P, H, S, width), torch.uint8, k_codes.device)

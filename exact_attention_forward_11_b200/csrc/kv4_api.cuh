@@ -16,7 +16,7 @@ attn_status kv4_check_cache(const void* k_codes, const void* k_sf, const void* v
   if (attn_status s = check_shape(B, Hkv, N); s != ATTN_OK) return s;
   if (num_pages < 1 || max_pages < 1 || page_size < 1) return ATTN_ERR_INVALID_ARG;
   if (k_exp < -32 || k_exp > 32 || v_exp < -32 || v_exp > 32) return ATTN_ERR_INVALID_ARG;
-  if (page_size > 65536 || (page_size & (page_size - 1)) != 0) return ATTN_ERR_UNSUPPORTED;
+  if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(max_pages) * page_size >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(num_pages) * Hkv >= (1ll << 32) / page_size) return ATTN_ERR_INVALID_ARG;
   if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_UNSUPPORTED;
@@ -168,7 +168,7 @@ attn_status attn_kv4_read(const void* k_codes, const void* k_sf, const void* v_c
 
 size_t attn_fwd_kv4_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {
   if (B < 1 || Hq < 1 || Hkv < 1 || N < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
-  if (page_size < 1 || page_size > 65536 || (page_size & (page_size - 1)) != 0 || max_pages < 1) return 0;
+  if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0 || max_pages < 1) return 0;
   return kv4_plan(B, Hq, Hkv, N, d, page_size, max_pages).workspace;
 }
 

@@ -16,8 +16,11 @@
 //    select per four pairs), since P V pairs values along the keys.
 //  * P leaves S^T with the keys along lanes' groups and is needed with the keys along t: one
 //    movmatrix per 8 keys x 8 rows.
-// Every warp streams its own 32 keys of each 256-key tile through a ring of cp.async stages
-// and keeps its own running maximum, sum and O; warps meet only where a segment ends. The
+// Every warp streams its own 32 keys of each 256-key tile through a ring of cp.async stages (a
+// 16-key group is contiguous in its page: nine 16-byte copies per lane and step, two address
+// computations per group and tensor; bulk copies issued by eight lanes cost more instructions,
+// since each lane's copy is issued in turn) and keeps its own running maximum, sum and O; warps meet
+// only where a segment ends. The
 // maximum moves only when a score exceeds it by more than 8 (log2 units), so most steps cost
 // one vote and no reduction across lanes; P <= 2^8 then, well inside f16.
 //
@@ -56,6 +59,7 @@ struct Kv4DecCfg {
   static constexpr int KSTEPS = D / 16;
   static constexpr int SMEM_Q = SMEM_ML + kDecWarps * ROWS * 8;
   static constexpr int SMEM_BYTES = SMEM_Q + (QREG ? 0 : KSTEPS * NT * 32 * 8);
+  static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 233472, "shared memory per SM");
 };
 
 struct Kv4AttnParams {
@@ -95,28 +99,42 @@ __device__ __forceinline__ long long warp_sum(long long v) {
   return v;
 }
 
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+// 16-byte asynchronous copy global -> shared; with `valid` false nothing is read and zeros are written
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-template <int BYTES>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(valid ? BYTES : 0), "n"(BYTES)
-               : "memory");
+__device__ __forceinline__ void cp_async_16z(uint32_t dst, const uint8_t* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// a f16x2 of one half of x
+__device__ __forceinline__ uint32_t splat_lo(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t splat_hi(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void mma_16816_zero(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 // whether one of the four scale bytes is a NaN
@@ -139,6 +157,21 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
   const uint32_t ring = smem0 + warp * C::STAGES * C::STAGE;
   asm volatile("griddepcontrol.launch_dependents;");
 
+  // Copies. Codes: lane takes bytes [16 lane, 16 lane + 16) of every 512 of a group's. Scales: lane
+  // takes 16 bytes of (tensor, group, piece); `grp` is also the group whose page it looks up.
+  constexpr int SFP = C::SF_ROW;                    // 16-byte pieces of a group's scales (16 rows)
+  const int grp = (lane / SFP) & 1;
+  const uint8_t* kptr = p.c.codes[0] + lane * 16;
+  const uint8_t* vptr = p.c.codes[1] + lane * 16;
+  const uint8_t* sptr = p.c.sf[(lane / (2 * SFP)) & 1] + (lane % SFP) * 16;
+  asm volatile("" : "+l"(kptr), "+l"(vptr), "+l"(sptr));    // kept in registers
+  const uint32_t kdst = ring + lane * 16;
+  const uint32_t sdst = ring + ((lane / (2 * SFP)) & 1 ? C::ST_VS : C::ST_KS) + (grp * SFP + lane % SFP) * 16;
+  const bool scopy = lane < 4 * SFP;
+  // S^T row g of an 8-row group is key g, with 2, 3 and 6, 7 swapped: K's 16-byte loads (two rows a
+  // phase) stay free of bank conflicts and V's 8-byte loads of the keys of rows 2 t meet two to
+  // a bank instead of four
+  const int gk = g ^ ((g >> 1) & 1), va = 2 * t + (t & 1), vb = 2 * t + 1 - (t & 1);
   // this CTA's run, and the (sequence, tiles before it) where it starts
   const int per_b = p.c.H * p.row_blocks;
   long long total = 0;
@@ -186,7 +219,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
     // ---- q fragments: lane (g, t) takes channels [D/4 t, D/4 (t+1)) of row g of each tile
     uint32_t qf[C::QREG ? NT : 1][C::KSTEPS][2];
     float cs[NT][2], m[NT][2], l[NT][2];
-    int lim[NT][2];                                 // last visible key of rows 2 t, 2 t + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = rb * ROWS + nt * 8 + g;
@@ -224,11 +256,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        cs[nt][j] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + j)) * p.scale_log2;
+        // (kept above zero: a masked score is -infinity and has to stay that)
+        cs[nt][j] = fmaxf(__shfl_sync(0xffffffffu, up, 4 * (2 * t + j)) * p.scale_log2, 1e-37f);
         m[nt][j] = -INFINITY;
         l[nt][j] = 0.f;
-        const int rr = rb * ROWS + nt * 8 + 2 * t + j;
-        lim[nt][j] = p.causal ? len - n + rr % p.N : len - 1;
       }
     }
     if constexpr (!C::QREG) __syncthreads();
@@ -243,56 +274,69 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
 
     // ---- the warp's pipeline over its 32-key steps
     const int* table = p.c.block_table + static_cast<long long>(b) * p.c.max_pages;
-    auto page_of = [&](int tt) {                    // page of this lane's key in tile tt
-      const int key = tt * kDecTile + warp * kDecKeys + lane;
-      return tt < t1 && key < len ? table[key >> p.c.page_shift] : 0;
+    const int steps_end = min(t1 * kDecTile, len);  // keys of this segment end here
+    const uint32_t slot_mask = (1u << p.c.page_shift) - 1u, hrow = static_cast<uint32_t>(h) << p.c.page_shift,
+                   page_rows = static_cast<uint32_t>(p.c.H) << p.c.page_shift;
+    auto page_of = [&](int base) {                  // page of this lane's group
+      const int key = base + 16 * grp;
+      return key < steps_end ? static_cast<uint32_t>(table[key >> p.c.page_shift]) : 0u;
     };
-    auto issue = [&](int tt, int page) {
-      if (tt < t1) {
-        const uint32_t st = ring + static_cast<uint32_t>((tt - t0) % C::STAGES) * C::STAGE;
-        const int key = tt * kDecTile + warp * kDecKeys + lane;
-        uint32_t row = 0u;
-        const bool ok = key < len && kv4_row(p.c, page, h, key, row);
-        // keys sit in K's stage in the order of the S^T rows they become: 16-key group, then
-        // slot 2 (k % 4) + k / 4 (+ 8 for its upper half), see V's loads
-        const int k16 = lane & 15;
-        const int kslot = (lane & 16) + (k16 & 8) + 2 * (k16 & 3) + ((k16 >> 2) & 1);
-        cp_async_small<C::SF_ROW>(st + C::ST_KS + kslot * C::SF_ROW, p.c.sf[0] + static_cast<size_t>(ok ? row : 0u) * C::SF_ROW, ok);
-        cp_async_small<C::SF_ROW>(st + C::ST_VS + lane * C::SF_ROW, p.c.sf[1] + static_cast<size_t>(ok ? row : 0u) * C::SF_ROW, ok);
-        constexpr int CH = C::CODE_ROW / 16;
-        const int ch = lane % CH;
-        const uint32_t mark = ok ? row : 0xFFFFFFFFu;
+    auto issue = [&](int base, uint32_t st, uint32_t pg) {
+      if (base < steps_end) {
+        const int key = base + 16 * grp;
+        const uint32_t row = pg * page_rows + (hrow + (static_cast<uint32_t>(key) & slot_mask));
+        if (__all_sync(0xffffffffu, pg < static_cast<uint32_t>(p.c.num_pages) && base + kDecKeys <= steps_end)) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int r = lane / CH + i * (32 / CH);
-          const uint32_t rr = __shfl_sync(0xffffffffu, mark, r);
-          const bool v = rr != 0xFFFFFFFFu;
-          const size_t off = static_cast<size_t>(v ? rr : 0u) * C::CODE_ROW + ch * 16;
-          const int r16 = r & 15;
-          const int slot = (r & 16) + (r16 & 8) + 2 * (r16 & 3) + ((r16 >> 2) & 1);
-          cp_async_16(st + slot * C::CODE_ROW + ch * 16, p.c.codes[0] + off, v);
-          const int vch = CH == 4 ? ch ^ (r & 2) : ch;       // (D = 128) spreads V's 8-byte loads over all banks
-          cp_async_16(st + C::ST_VC + r * C::CODE_ROW + vch * 16, p.c.codes[1] + off, v);
+          for (int gr = 0; gr < 2; ++gr) {
+            const uint32_t rr = __shfl_sync(0xffffffffu, row, gr * SFP);
+            const uint8_t* ks = kptr + static_cast<size_t>(rr) * C::CODE_ROW;
+            const uint8_t* vs = vptr + static_cast<size_t>(rr) * C::CODE_ROW;
+#pragma unroll
+            for (int i = 0; i < 16 * C::CODE_ROW; i += 512) {
+              cp_async_16(kdst + st + gr * 16 * C::CODE_ROW + i, ks + i);
+              cp_async_16(kdst + st + C::ST_VC + gr * 16 * C::CODE_ROW + i, vs + i);
+            }
+          }
+          if (scopy) cp_async_16(sdst + st, sptr + static_cast<size_t>(row) * C::SF_ROW);
+        } else {
+          // a sequence's last step, or a page outside the cache: what is not there is zero (keys behind
+          // the end inside a copied group are masked, and their scales looked at, below)
+          uint32_t unused;
+          const bool mine = key < steps_end && kv4_row(p.c, static_cast<int>(pg), h, key, unused);
+#pragma unroll
+          for (int gr = 0; gr < 2; ++gr) {
+            const bool v = __shfl_sync(0xffffffffu, mine, gr * SFP);
+            const uint32_t rr = __shfl_sync(0xffffffffu, mine ? row : 0u, gr * SFP);
+#pragma unroll
+            for (int i = 0; i < 16 * C::CODE_ROW; i += 512) {
+              cp_async_16z(kdst + st + gr * 16 * C::CODE_ROW + i, kptr + static_cast<size_t>(rr) * C::CODE_ROW + i, v);
+              cp_async_16z(kdst + st + C::ST_VC + gr * 16 * C::CODE_ROW + i,
+                           vptr + static_cast<size_t>(rr) * C::CODE_ROW + i, v);
+            }
+          }
+          if (scopy) cp_async_16z(sdst + st, sptr + static_cast<size_t>(mine ? row : 0u) * C::SF_ROW, mine);
         }
       }
       cp_async_commit();
     };
-    int page = page_of(t0);
+    const int base0 = t0 * kDecTile + warp * kDecKeys;
+    uint32_t page = page_of(base0);
 #pragma unroll
     for (int s = 0; s < C::STAGES - 1; ++s) {
-      const int nx = page_of(t0 + s + 1);
-      issue(t0 + s, page);
+      const uint32_t nx = page_of(base0 + (s + 1) * kDecTile);
+      issue(base0 + s * kDecTile, s * C::STAGE, page);
       page = nx;
     }
-    for (int tt = t0; tt < t1; ++tt) {
+    uint32_t rd = 0, wr = (C::STAGES - 1) * C::STAGE;      // offsets of the stage to use and of the one to fill
+    for (int base = base0; base < steps_end; base += kDecTile) {
       cp_async_wait<C::STAGES - 2>();
       __syncwarp();
-      const int nx = page_of(tt + C::STAGES);
-      issue(tt + C::STAGES - 1, page);
+      const uint32_t nx = page_of(base + C::STAGES * kDecTile);
+      issue(base + (C::STAGES - 1) * kDecTile, wr, page);
       page = nx;
-      const uint8_t* st = smem_raw + (ring - smem0) + static_cast<uint32_t>((tt - t0) % C::STAGES) * C::STAGE;
-      const int base = tt * kDecTile + warp * kDecKeys;
-      if (base >= len) continue;
+      wr = rd;
+      const uint8_t* st = smem_raw + (ring - smem0) + rd;
+      rd = rd == (C::STAGES - 1) * C::STAGE ? 0u : rd + C::STAGE;
       // ---- S^T of 32 keys
       float s[2][NT][4];
 #pragma unroll
@@ -301,7 +345,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
         uint32_t ks[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int slot = 16 * mt + 8 * j + g;
+          const int slot = 16 * mt + 8 * j + gk;
           const uint8_t* a = st + slot * C::CODE_ROW + t * (D / 8);
           if constexpr (D == 128) {
             const uint4 x = *reinterpret_cast<const uint4*>(a);
@@ -315,16 +359,12 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
           }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[mt][nt][j] = 0.f;
-#pragma unroll
         for (int wd = 0; wd < D / 32; ++wd) {       // a word: 8 channels, two k-steps
           uint32_t f[2][4];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             f16x2_from_e2m1x8(kw[j][wd], f[j]);
-            const uint32_t sc = D == 128 ? __byte_perm(ks[j], 0u, wd < 2 ? 0x1010 : 0x3232) : ks[j];
+            const uint32_t sc = D == 128 ? (wd < 2 ? splat_lo(ks[j]) : splat_hi(ks[j])) : ks[j];
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[j][i] = hmul2(f[j][i], sc);
           }
@@ -334,22 +374,16 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
             const int k = 2 * wd + hf;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              if constexpr (C::QREG) {
-                mma_16816(s[mt][nt], a, qf[nt][k][0], qf[nt][k][1]);
-              } else {
-                const uint2 qq = *reinterpret_cast<const uint2*>(smem_raw + C::SMEM_Q + ((k * NT + nt) * 32 + lane) * 8);
+              const uint2 qq = C::QREG ? make_uint2(qf[C::QREG ? nt : 0][k][0], qf[C::QREG ? nt : 0][k][1])
+                                       : *reinterpret_cast<const uint2*>(smem_raw + C::SMEM_Q + ((k * NT + nt) * 32 + lane) * 8);
+              if (k == 0)
+                mma_16816_zero(s[mt][nt], a, qq.x, qq.y);
+              else
                 mma_16816(s[mt][nt], a, qq.x, qq.y);
-              }
             }
           }
         }
       }
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[mt][nt][j] *= cs[nt][j & 1];
       // ---- masks: only steps that some row does not see to their end
       uint32_t vnan = 0u;                           // (masked steps) keys whose values hold a NaN
       if (base + kDecKeys - 1 > lim_all) {
@@ -362,15 +396,18 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
         }
         vnan = __ballot_sync(0xffffffffu, bad);
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int k = 16 * mt + 8 * (j >> 1) + (g >> 1) + 4 * (g & 1);   // the key of this S^T row
+          for (int j = 0; j < 2; ++j) {
+            const int rr = rb * ROWS + nt * 8 + 2 * t + j;
+            const int lim = (p.causal ? len - n + rr % p.N : len - 1) - base;   // the row's last visible key
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int i = 0; i < 4; ++i) {
+              const int k = 8 * i + gk;             // the key of this S^T row
+              float& x = s[i >> 1][nt][2 * (i & 1) + j];
               // a NaN value reaches the rows that see it through their scores, and no other
-              if ((vnan >> k) & 1u) s[mt][nt][j] = __int_as_float(0x7FC00000);
-              if (base + k > lim[nt][j & 1]) s[mt][nt][j] = -INFINITY;
+              if ((vnan >> k) & 1u) x = __int_as_float(0x7FC00000);
+              if (k > lim) x = -INFINITY;
             }
           }
       }
@@ -381,7 +418,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          mx[nt][j] = fmaxf(fmaxf(s[0][nt][j], s[0][nt][j + 2]), fmaxf(s[1][nt][j], s[1][nt][j + 2]));
+          mx[nt][j] = cs[nt][j] * fmaxf(fmaxf(s[0][nt][j], s[0][nt][j + 2]), fmaxf(s[1][nt][j], s[1][nt][j + 2]));
           grow = grow || mx[nt][j] > m[nt][j] + 8.f;
         }
       if (__any_sync(0xffffffffu, grow)) {
@@ -411,29 +448,34 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const float p0 = b200::ex2_approx(s[mt][nt][2 * hf] - m0), p1 = b200::ex2_approx(s[mt][nt][2 * hf + 1] - m1);
+            const float p0 = b200::ex2_approx(fmaf(s[mt][nt][2 * hf], cs[nt][0], -m0));
+            const float p1 = b200::ex2_approx(fmaf(s[mt][nt][2 * hf + 1], cs[nt][1], -m1));
             l[nt][0] += p0;
             l[nt][1] += p1;
             pb[mt][nt][hf] = movmatrix(b200::pack_f16x2(p0, p1));
           }
       }
-      // ---- O^T += V^^T P^T: S^T rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 are keys t, t + 4, t + 8, t + 12
+      // ---- O^T += V^^T P^T over the keys of S^T rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         uint32_t vw[4][D / 64];
         uint32_t by[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = 16 * mt + t + 4 * i;
+          const int r = 16 * mt + 8 * (i >> 1) + ((i & 1) ? vb : va);
           if constexpr (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2*>(st + C::ST_VC + r * 64 + (((g >> 1) ^ (r & 2)) << 4) + (g & 1) * 8);
+            const uint2 x = *reinterpret_cast<const uint2*>(st + C::ST_VC + r * 64 + g * 8);
             vw[i][0] = x.x, vw[i][1] = x.y;
             by[i] = st[C::ST_VS + r * 8 + g];
           } else {
             vw[i][0] = *reinterpret_cast<const uint32_t*>(st + C::ST_VC + r * 32 + g * 4);
             by[i] = st[C::ST_VS + r * 4 + (g >> 1)];
           }
-          if (vnan != 0u && (by[i] & 0x7Fu) == 0x7Fu) by[i] = 0u;
+        }
+        if (vnan != 0u) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((by[i] & 0x7Fu) == 0x7Fu) by[i] = 0u;
         }
         uint32_t vs[2];
 #pragma unroll
@@ -441,7 +483,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
           vs[pr] = b200::f16x2_from_e4m3x2(static_cast<uint16_t>(by[2 * pr] | (by[2 * pr + 1] << 8)));
 #pragma unroll
         for (int wd = 0; wd < D / 64; ++wd) {
-          uint32_t ev[2][4], od[2][4];              // f16 pairs (key, key + 4) of even and odd channels
+          uint32_t ev[2][4], od[2][4];              // f16 pairs (two keys) of even and odd channels
 #pragma unroll
           for (int pr = 0; pr < 2; ++pr) {
             const uint32_t wa = vw[2 * pr][wd], wb = vw[2 * pr + 1][wd];
@@ -462,8 +504,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
         }
       }
     }
-    cp_async_wait<0>();
-
     // ---- the segment ends: the warps' results meet in shared memory
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -471,6 +511,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int sft = 4; sft < 32; sft <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], sft);
+    cp_async_wait<0>();
     __syncthreads();
     float* mo = reinterpret_cast<float*>(smem_raw);
     float2* ml = reinterpret_cast<float2*>(smem_raw + C::SMEM_ML);

@@ -27,7 +27,7 @@
  *   block_table      : [B, max_pages] int32; position p of sequence b lies in page
  *                      block_table[b, p / page_size], slot p % page_size.
  *   seq_lens         : [B] int32 tokens of each sequence in the cache, 0 or more.
- * page_size is a power of two, at most 65536; max_pages * page_size < 2^31;
+ * page_size is a power of two from 16 to 65536 (else ATTN_ERR_UNSUPPORTED); max_pages * page_size < 2^31;
  * num_pages * Hkv * page_size < 2^32; d is 64 or 128 (else ATTN_ERR_UNSUPPORTED);
  * |k_exp|, |v_exp| <= 32. dtype (of k, v, q, o) is ATTN_BF16 or ATTN_FP16.
  *

@@ -21,7 +21,7 @@ FWD = dict(q=FAKE, kc=FAKE, ks=FAKE, vc=FAKE, vs=FAKE, bt=FAKE, sl=FAKE, ql=None
            dtype=0, stream=None)
 # (changed arguments, status) that all three calls share
 SHARED = [(dict(B=0), 1), (dict(Hkv=0), 1), (dict(N=-1), 1), (dict(pages=0), 1), (dict(maxp=0), 1), (dict(page=0), 1),
-          (dict(page=24), 2), (dict(page=1 << 17), 2), (dict(d=96), 2), (dict(d=256), 2), (dict(dtype=2), 2),
+          (dict(page=24), 2), (dict(page=8), 2), (dict(page=1 << 17), 2), (dict(d=96), 2), (dict(d=256), 2), (dict(dtype=2), 2),
           (dict(ke=33), 1), (dict(ve=-33), 1), (dict(page=65536, maxp=1 << 15), 1),
           (dict(pages=1 << 30, page=16), 1)]
 

@@ -104,7 +104,7 @@ def check_attention(o, lse, q, pg, lens, qlens, causal, scale=None, rows=None):
 @pytest.mark.parametrize("d,page,dt,N,lens,new,exps", [
     (128, 16, torch.bfloat16, 1, [1], [1], (0, 0)),                       # the first token of a sequence
     (128, 16, torch.float16, 1, [17, 16, 33], [1, 1, 1], (0, 0)),         # either side of a page border
-    (64, 1, torch.bfloat16, 5, [5, 9], [5, 2], (-3, 2)),                  # a page per token
+    (64, 16, torch.bfloat16, 5, [5, 19], [5, 5], (-3, 2)),                # across a page border
     (64, 32, torch.float16, 37, [37, 101, 0], [37, 20, 0], (0, -5)),      # ragged, an empty sequence
     (128, 64, torch.bfloat16, 130, [130, 255], [0, 130], (4, 0)),         # nothing new for one of them
 ])
@@ -170,7 +170,7 @@ def test_append_at_the_rounding_borders(cuda_lib, dt):
 @pytest.mark.parametrize("d,page,dt,lens,starts,N,exps", [
     (128, 16, torch.bfloat16, [1], None, 1, (0, 0)),
     (128, 16, torch.float16, [40, 17, 0], [3, 16, 0], 30, (0, 0)),         # past the end, nothing at all
-    (64, 8, torch.bfloat16, [100, 63], [99, 0], 64, (-20, 17)),
+    (64, 16, torch.bfloat16, [100, 63], [99, 0], 64, (-20, 17)),
     (64, 128, torch.float16, [300, 129], [200, 128], 100, (1, -3)),
 ])
 def test_read_is_exact(cuda_lib, d, page, dt, lens, starts, N, exps):
@@ -194,7 +194,7 @@ ATTN_CASES = [
     (128, 8, 2, 16, torch.float16, 1, [7, 33, 300], None, False, (0, 0)),
     (64, 3, 3, 32, torch.bfloat16, 1, [0, 64, 129, 513], None, True, (0, -4)),          # an empty sequence, no grouping
     (128, 16, 1, 64, torch.bfloat16, 1, [1000, 257], None, False, (-6, 3)),
-    (64, 14, 2, 1, torch.float16, 1, [70, 31], None, False, (0, 0)),                    # a page per token, 7 to a head
+    (64, 14, 2, 16, torch.float16, 1, [70, 31], None, False, (0, 0)),                   # 7 to a head
     (128, 8, 2, 16, torch.bfloat16, 3, [3, 50, 600], None, True, (0, 0)),
     (128, 8, 1, 16, torch.float16, 4, [5, 900], [4, 2], True, (0, 0)),                  # padded queries
     (64, 6, 2, 16, torch.bfloat16, 5, [40, 3, 700], [5, 5, 0], True, (0, 0)),           # more queries than keys
@@ -202,7 +202,7 @@ ATTN_CASES = [
     (128, 4, 2, 16, torch.bfloat16, 130, [130, 515], [130, 129], True, (0, 0)),
     (64, 4, 1, 128, torch.float16, 100, [777, 100], [100, 100], False, (2, 0)),
     (128, 5, 5, 16, torch.bfloat16, 257, [300], None, True, (0, 0)),
-    (64, 8, 8, 8, torch.bfloat16, 65, [65, 64, 200], [65, 64, 1], True, (0, 0)),
+    (64, 8, 8, 16, torch.bfloat16, 65, [65, 64, 200], [65, 64, 1], True, (0, 0)),
     (128, 2, 1, 65536, torch.float16, 200, [1025], None, True, (0, 0)),                 # one page holds everything
 ]
 
