@@ -566,7 +566,7 @@ class KV4Cache:
     above 2000."""
 
     __slots__ = ("k_codes", "k_sf", "v_codes", "v_sf", "k_exp", "v_exp", "num_pages", "heads", "page_size", "d",
-                 "device", "_ptrs")
+                 "device", "_ptrs", "_need")
 
     def __init__(self, k_codes, k_sf, v_codes, v_sf, k_exp=0, v_exp=0):
         import torch
@@ -582,6 +582,7 @@ class KV4Cache:
         self.k_exp, self.v_exp = int(k_exp), int(v_exp)
         self.num_pages, self.heads, self.page_size, self.d, self.device = P, H, S, 2 * half, k_codes.device
         self._ptrs = tuple(t.data_ptr() for t in (k_codes, k_sf, v_codes, v_sf))
+        self._need = {}      # workspace bytes of forward_kv4 by (B, Hq, N, max_pages)
 
     @classmethod
     def allocate(cls, num_pages, heads, page_size, d, k_exp=0, v_exp=0, device="cuda"):
@@ -625,22 +626,23 @@ class _kv4_place:
     __slots__ = ("device", "stream", "ctx")
 
     def __init__(self, device, stream):
-        self.device, self.stream, self.ctx = device, stream, []
+        self.device, self.stream, self.ctx = device, stream, ()
 
     def __enter__(self):
         import torch
-        if self.device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(self.device))
-            self.ctx[-1].__enter__()
-        if self.stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        self.ctx.append(torch.cuda.stream(self.stream))
-        self.ctx[-1].__enter__()
-        return self.stream.cuda_stream
+        index = self.device.index
+        if self.stream is None and index == torch._C._cuda_getDevice():
+            return torch._C._cuda_getCurrentRawStream(index)
+        self.ctx = [torch.cuda.device(self.device)]
+        if self.stream is not None:
+            self.ctx.append(torch.cuda.stream(self.stream))
+        for c in self.ctx:
+            c.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
 
     def __exit__(self, *exc):
-        while self.ctx:
-            self.ctx.pop().__exit__(*exc)
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
 
 
 def kv4_append(cache, k, v, block_table, seq_lens, new_lens=None, stream=None, check=False):
@@ -715,7 +717,11 @@ def forward_kv4(q, cache, block_table, seq_lens, q_lens=None, causal=False, scal
         if lse is not None:
             _expect(lse, "lse", (B, Hq, N), torch.float32, q.device)
         max_pages = block_table.shape[1]
-        need = attn_fwd_kv4_workspace_bytes(B, Hq, cache.heads, N, cache.d, cache.page_size, max_pages)
+        sizes = (B, Hq, N, max_pages)
+        need = cache._need.get(sizes)
+        if need is None:
+            need = attn_fwd_kv4_workspace_bytes(B, Hq, cache.heads, N, cache.d, cache.page_size, max_pages)
+            cache._need[sizes] = need
         if workspace is None:
             if need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)

@@ -52,9 +52,11 @@ struct Kv4DecCfg {
   static constexpr int ST_VC = kDecKeys * CODE_ROW, ST_KS = 2 * kDecKeys * CODE_ROW,
                        ST_VS = ST_KS + kDecKeys * SF_ROW, STAGE = ST_VS + kDecKeys * SF_ROW;
   static constexpr int RING = kDecWarps * STAGES * STAGE;
-  static constexpr int O_LD = D + 8;               // floats between rows of a warp's O in the merge buffer
-  static constexpr int MERGE = kDecWarps * ROWS * O_LD * 4;
-  static constexpr int SMEM_ML = RING > MERGE ? RING : MERGE;            // [warps][ROWS] (max, sum)
+  // where a segment ends, a warp leaves its O in NT free stages of its ring, 8 rows in each, while the
+  // next segment's first copies fill the others
+  static constexpr int O_LD = D + 8;               // floats between rows of a warp's O
+  static_assert(8 * O_LD * 4 <= STAGE && STAGES >= NT + 2, "merge stages");
+  static constexpr int SMEM_ML = RING;             // [warps][ROWS] (max, sum)
   static constexpr bool QREG = NT <= 2;            // q fragments in registers, else in shared memory
   static constexpr int KSTEPS = D / 16;
   static constexpr int SMEM_Q = SMEM_ML + kDecWarps * ROWS * 8;
@@ -172,18 +174,27 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
   // phase) stay free of bank conflicts and V's 8-byte loads of the keys of rows 2 t meet two to
   // a bank instead of four
   const int gk = g ^ ((g >> 1) & 1), va = 2 * t + (t & 1), vb = 2 * t + 1 - (t & 1);
-  // this CTA's run, and the (sequence, tiles before it) where it starts
+  // this CTA's run, and the (sequence, tiles before it) where it starts. Up to 32 sequences' lengths
+  // stay in the lanes; more are read again.
   const int per_b = p.c.H * p.row_blocks;
+  const bool few = p.c.B <= 32;
+  int my_len = 0, my_n = 0;                         // of sequence `lane`, if few
   long long total = 0;
-  for (int b = lane; b < p.c.B; b += 32) total += kv4_tiles(p, b);
-  const Kv4Runs runs(warp_sum(total) * per_b, p.ctas);
+  for (int i = lane; i < p.c.B; i += 32) {
+    my_len = kv4_len(p.c, i);
+    my_n = kv4_qlen(p, i);
+    total += my_n == 0 ? 0 : (my_len + kDecTile - 1) / kDecTile;
+  }
+  const long long my_units = total * per_b;
+  const Kv4Runs runs(warp_sum(my_units), p.ctas);
   if (static_cast<int>(blockIdx.x) >= runs.n) return;
   long long u = runs.start(blockIdx.x);
-  const long long u_end = runs.start(blockIdx.x + 1);
+  const long long u_begin = u, u_end = runs.start(blockIdx.x + 1);
   int b = 0;
   long long b_first = 0;                            // first unit of sequence b
   for (int b0 = 0;; b0 += 32) {
-    const long long mine = b0 + lane < p.c.B ? static_cast<long long>(kv4_tiles(p, b0 + lane)) * per_b : 0;
+    const long long mine =
+        few ? my_units : (b0 + lane < p.c.B ? static_cast<long long>(kv4_tiles(p, b0 + lane)) * per_b : 0);
     long long incl = mine;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
@@ -199,37 +210,123 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
     }
     b_first += __shfl_sync(0xffffffffu, incl, 31);
   }
-  const long long u_begin = u;
+  const int R = p.Hq / p.c.H * p.N;
+  const uint32_t slot_mask = (1u << p.c.page_shift) - 1u, page_rows = static_cast<uint32_t>(p.c.H) << p.c.page_shift;
 
-  while (u < u_end) {
-    int T = kv4_tiles(p, b);
-    while (u >= b_first + static_cast<long long>(T) * per_b) {   // sequences without tiles are passed over
-      b_first += static_cast<long long>(T) * per_b;
-      T = kv4_tiles(p, ++b);
+  // the segment being worked on: tiles [t0, t1) of T of (b, h, row block rb)
+  int T, h, rb, t0, t1, len, n, steps_end, base0;
+  uint32_t hrow;
+  long long item_first;
+  size_t row0;                                      // rows of (b, h) are contiguous in q and o
+  const int* table;
+  auto find_segment = [&]() {                       // the one that starts at unit u
+    for (;;) {
+      len = few ? __shfl_sync(0xffffffffu, my_len, b) : kv4_len(p.c, b);
+      n = few ? __shfl_sync(0xffffffffu, my_n, b) : kv4_qlen(p, b);
+      T = n == 0 ? 0 : (len + kDecTile - 1) / kDecTile;
+      if (u < b_first + static_cast<long long>(T) * per_b) break;
+      b_first += static_cast<long long>(T) * per_b;  // (sequences without tiles are passed over)
+      ++b;
     }
-    const int item = static_cast<int>((u - b_first) / T);
-    const long long item_first = b_first + static_cast<long long>(item) * T;
-    const int h = item / p.row_blocks, rb = item % p.row_blocks;
-    const int t0 = static_cast<int>(u - item_first);
-    const int t1 = static_cast<int>(min(static_cast<long long>(T), u_end - item_first));
-    const int len = kv4_len(p.c, b), n = kv4_qlen(p, b);
-    const int R = p.Hq / p.c.H * p.N;
-    const size_t row0 = (static_cast<size_t>(b) * p.c.H + h) * R;      // rows of (b, h) are contiguous in q and o
+    const int item = static_cast<int>(static_cast<uint32_t>(u - b_first) / static_cast<uint32_t>(T));
+    item_first = b_first + static_cast<long long>(item) * T;
+    h = item / p.row_blocks, rb = item % p.row_blocks;
+    t0 = static_cast<int>(u - item_first);
+    t1 = static_cast<int>(min(static_cast<long long>(T), u_end - item_first));
+    row0 = (static_cast<size_t>(b) * p.c.H + h) * R;
+    table = p.c.block_table + static_cast<long long>(b) * p.c.max_pages;
+    steps_end = min(t1 * kDecTile, len);            // its keys end here
+    base0 = t0 * kDecTile + warp * kDecKeys;        // this warp's first step
+    hrow = static_cast<uint32_t>(h) << p.c.page_shift;
+  };
 
-    // ---- q fragments: lane (g, t) takes channels [D/4 t, D/4 (t+1)) of row g of each tile
+  // ---- a warp's pipeline over its 32-key steps
+  auto page_of = [&](int base) {                  // page of this lane's group
+    const int key = base + 16 * grp;
+    return key < steps_end ? static_cast<uint32_t>(table[key >> p.c.page_shift]) : 0u;
+  };
+  auto issue = [&](int base, uint32_t st, uint32_t pg) {
+    if (base < steps_end) {
+      const int key = base + 16 * grp;
+      const uint32_t row = pg * page_rows + (hrow + (static_cast<uint32_t>(key) & slot_mask));
+      if (__all_sync(0xffffffffu, pg < static_cast<uint32_t>(p.c.num_pages) && base + kDecKeys <= steps_end)) {
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) {
+          const uint32_t rr = __shfl_sync(0xffffffffu, row, gr * SFP);
+          const uint8_t* ks = kptr + static_cast<size_t>(rr) * C::CODE_ROW;
+          const uint8_t* vs = vptr + static_cast<size_t>(rr) * C::CODE_ROW;
+#pragma unroll
+          for (int i = 0; i < 16 * C::CODE_ROW; i += 512) {
+            cp_async_16(kdst + st + gr * 16 * C::CODE_ROW + i, ks + i);
+            cp_async_16(kdst + st + C::ST_VC + gr * 16 * C::CODE_ROW + i, vs + i);
+          }
+        }
+        if (scopy) cp_async_16(sdst + st, sptr + static_cast<size_t>(row) * C::SF_ROW);
+      } else {
+        // a sequence's last step, or a page outside the cache: what is not there is zero (keys behind
+        // the end inside a copied group are masked, and their scales looked at, below)
+        uint32_t unused;
+        const bool mine = key < steps_end && kv4_row(p.c, static_cast<int>(pg), h, key, unused);
+#pragma unroll
+        for (int gr = 0; gr < 2; ++gr) {
+          const bool v = __shfl_sync(0xffffffffu, mine, gr * SFP);
+          const uint32_t rr = __shfl_sync(0xffffffffu, mine ? row : 0u, gr * SFP);
+#pragma unroll
+          for (int i = 0; i < 16 * C::CODE_ROW; i += 512) {
+            cp_async_16z(kdst + st + gr * 16 * C::CODE_ROW + i, kptr + static_cast<size_t>(rr) * C::CODE_ROW + i, v);
+            cp_async_16z(kdst + st + C::ST_VC + gr * 16 * C::CODE_ROW + i,
+                         vptr + static_cast<size_t>(rr) * C::CODE_ROW + i, v);
+          }
+        }
+        if (scopy) cp_async_16z(sdst + st, sptr + static_cast<size_t>(mine ? row : 0u) * C::SF_ROW, mine);
+      }
+    }
+    cp_async_commit();
+  };
+  auto after = [](uint32_t st) { return st == (C::STAGES - 1) * C::STAGE ? 0u : st + C::STAGE; };
+  uint32_t rd = 0, wr = 0;                          // offsets of the stage to use and of the one to fill
+  uint32_t page = 0;                                // of the step to issue next
+  int next_base = 0;
+  auto issue_next = [&](int count) {
+    for (int i = 0; i < count; ++i) {
+      const uint32_t nx = page_of(next_base + kDecTile);
+      issue(next_base, wr, page);
+      page = nx;
+      next_base += kDecTile;
+      wr = after(wr);
+    }
+  };
+  auto start_segment = [&](int stages) {            // its first copies
+    next_base = base0;
+    page = page_of(base0);
+    issue_next(stages);
+  };
+  // q: lane (g, t) takes channels [D/4 t, D/4 (t+1)) of row g of each tile
+  // (NT = 1: loaded ahead, under the copies' latency)
+  constexpr bool AHEAD = NT == 1;
+  uint32_t qw[D / 8];
+  auto load_q = [&](int nt) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int r = rb * ROWS + nt * 8 + g;
+      const uint4 x = r < R ? reinterpret_cast<const uint4*>(p.q + ((row0 + r) * D + t * (D / 4)) * 2)[i]
+                            : make_uint4(0u, 0u, 0u, 0u);
+      qw[4 * i] = x.x, qw[4 * i + 1] = x.y, qw[4 * i + 2] = x.z, qw[4 * i + 3] = x.w;
+    }
+  };
+
+  find_segment();
+  start_segment(C::STAGES - 1);
+  if (AHEAD) load_q(0);
+  for (;;) {
+    // ---- q fragments
     uint32_t qf[C::QREG ? NT : 1][C::KSTEPS][2];
     float cs[NT][2], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = rb * ROWS + nt * 8 + g;
-      uint32_t w[D / 8];
+      if (!AHEAD) load_q(nt);
+      uint32_t (&w)[D / 8] = qw;
       float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 x = r < R ? reinterpret_cast<const uint4*>(p.q + ((row0 + r) * D + t * (D / 4)) * 2)[i]
-                              : make_uint4(0u, 0u, 0u, 0u);
-        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-      }
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         const float2 f = f32x2_from_16<F16>(w[i]);
@@ -272,71 +369,15 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
 
-    // ---- the warp's pipeline over its 32-key steps
-    const int* table = p.c.block_table + static_cast<long long>(b) * p.c.max_pages;
-    const int steps_end = min(t1 * kDecTile, len);  // keys of this segment end here
-    const uint32_t slot_mask = (1u << p.c.page_shift) - 1u, hrow = static_cast<uint32_t>(h) << p.c.page_shift,
-                   page_rows = static_cast<uint32_t>(p.c.H) << p.c.page_shift;
-    auto page_of = [&](int base) {                  // page of this lane's group
-      const int key = base + 16 * grp;
-      return key < steps_end ? static_cast<uint32_t>(table[key >> p.c.page_shift]) : 0u;
-    };
-    auto issue = [&](int base, uint32_t st, uint32_t pg) {
-      if (base < steps_end) {
-        const int key = base + 16 * grp;
-        const uint32_t row = pg * page_rows + (hrow + (static_cast<uint32_t>(key) & slot_mask));
-        if (__all_sync(0xffffffffu, pg < static_cast<uint32_t>(p.c.num_pages) && base + kDecKeys <= steps_end)) {
-#pragma unroll
-          for (int gr = 0; gr < 2; ++gr) {
-            const uint32_t rr = __shfl_sync(0xffffffffu, row, gr * SFP);
-            const uint8_t* ks = kptr + static_cast<size_t>(rr) * C::CODE_ROW;
-            const uint8_t* vs = vptr + static_cast<size_t>(rr) * C::CODE_ROW;
-#pragma unroll
-            for (int i = 0; i < 16 * C::CODE_ROW; i += 512) {
-              cp_async_16(kdst + st + gr * 16 * C::CODE_ROW + i, ks + i);
-              cp_async_16(kdst + st + C::ST_VC + gr * 16 * C::CODE_ROW + i, vs + i);
-            }
-          }
-          if (scopy) cp_async_16(sdst + st, sptr + static_cast<size_t>(row) * C::SF_ROW);
-        } else {
-          // a sequence's last step, or a page outside the cache: what is not there is zero (keys behind
-          // the end inside a copied group are masked, and their scales looked at, below)
-          uint32_t unused;
-          const bool mine = key < steps_end && kv4_row(p.c, static_cast<int>(pg), h, key, unused);
-#pragma unroll
-          for (int gr = 0; gr < 2; ++gr) {
-            const bool v = __shfl_sync(0xffffffffu, mine, gr * SFP);
-            const uint32_t rr = __shfl_sync(0xffffffffu, mine ? row : 0u, gr * SFP);
-#pragma unroll
-            for (int i = 0; i < 16 * C::CODE_ROW; i += 512) {
-              cp_async_16z(kdst + st + gr * 16 * C::CODE_ROW + i, kptr + static_cast<size_t>(rr) * C::CODE_ROW + i, v);
-              cp_async_16z(kdst + st + C::ST_VC + gr * 16 * C::CODE_ROW + i,
-                           vptr + static_cast<size_t>(rr) * C::CODE_ROW + i, v);
-            }
-          }
-          if (scopy) cp_async_16z(sdst + st, sptr + static_cast<size_t>(mine ? row : 0u) * C::SF_ROW, mine);
-        }
-      }
-      cp_async_commit();
-    };
-    const int base0 = t0 * kDecTile + warp * kDecKeys;
-    uint32_t page = page_of(base0);
-#pragma unroll
-    for (int s = 0; s < C::STAGES - 1; ++s) {
-      const uint32_t nx = page_of(base0 + (s + 1) * kDecTile);
-      issue(base0 + s * kDecTile, s * C::STAGE, page);
-      page = nx;
-    }
-    uint32_t rd = 0, wr = (C::STAGES - 1) * C::STAGE;      // offsets of the stage to use and of the one to fill
     for (int base = base0; base < steps_end; base += kDecTile) {
       cp_async_wait<C::STAGES - 2>();
       __syncwarp();
       const uint32_t nx = page_of(base + C::STAGES * kDecTile);
       issue(base + (C::STAGES - 1) * kDecTile, wr, page);
       page = nx;
-      wr = rd;
+      wr = rd;                                      // the stage to fill is the one used last
       const uint8_t* st = smem_raw + (ring - smem0) + rd;
-      rd = rd == (C::STAGES - 1) * C::STAGE ? 0u : rd + C::STAGE;
+      rd = after(rd);
       // ---- S^T of 32 keys
       float s[2][NT][4];
 #pragma unroll
@@ -504,35 +545,56 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
         }
       }
     }
-    // ---- the segment ends: the warps' results meet in shared memory
+    // ---- the segment ends: the next one's first copies go out, and the warps' results meet in shared
+    // memory. Copies that the loop issued past the segment's end were empty, so `rd` is the next stage.
+    cp_async_wait<0>();
+    __syncwarp();
+    if (base0 + (t1 - t0 - 1) * kDecTile >= steps_end) rd = after(rd);   // the last tile ends before this warp's
+                                                    // keys: every warp's ring stands at the same stage
+    const bool whole = t0 == 0 && t1 == T;
+    const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
+    const int out_rb = rb, out_n = n;
+    const size_t out_row0 = row0;
+    u = item_first + t1;
+    wr = rd;
+    const bool more = u < u_end;
+    if (more) {
+      find_segment();
+      start_segment(C::STAGES - NT);
+    } else {
+      for (int i = 0; i < C::STAGES - NT; ++i) wr = after(wr);
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int sft = 4; sft < 32; sft <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], sft);
-    cp_async_wait<0>();
-    __syncthreads();
-    float* mo = reinterpret_cast<float*>(smem_raw);
     float2* ml = reinterpret_cast<float2*>(smem_raw + C::SMEM_ML);
+    uint32_t mst[NT];                               // the stages that take O
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mst[nt] = nt == 0 ? wr : after(mst[nt > 0 ? nt - 1 : 0]);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int r = nt * 8 + 2 * t + j;
-        if (g == 0) ml[warp * ROWS + r] = make_float2(m[nt][j], l[nt][j]);
-        float* dst = mo + (warp * ROWS + r) * C::O_LD + g * (D / 8);
+        const int r = 2 * t + j;
+        if (g == 0) ml[warp * ROWS + nt * 8 + r] = make_float2(m[nt][j], l[nt][j]);
+        float* dst = reinterpret_cast<float*>(smem_raw + warp * C::STAGES * C::STAGE + mst[nt]) + r * C::O_LD + g * (D / 8);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
           *reinterpret_cast<float4*>(dst + 4 * i) =
               make_float4(o[nt][2 * i][j], o[nt][2 * i][j + 2], o[nt][2 * i + 1][j], o[nt][2 * i + 1][j + 2]);
       }
+    if (AHEAD && more) load_q(0);
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == T;
-    const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
     constexpr int V4 = D / 4;                       // float4 per row
     for (int i = tid; i < ROWS * V4; i += kDecWarps * 32) {
       const int r = i / V4, d4 = i % V4;
+      uint32_t mst_r = mst[0];
+#pragma unroll
+      for (int nt = 1; nt < NT; ++nt)
+        if ((r >> 3) == nt) mst_r = mst[nt];
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ml[w * ROWS + r].x);
@@ -543,26 +605,27 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
       for (int w = 0; w < kDecWarps; ++w) {
         const float2 x = ml[w * ROWS + r];
         const float f = b200::ex2_approx(x.x - Mu);
-        const float4 v = *reinterpret_cast<const float4*>(mo + (w * ROWS + r) * C::O_LD + 4 * d4);
+        const float4 v = *reinterpret_cast<const float4*>(smem_raw + w * C::STAGES * C::STAGE + mst_r + ((r & 7) * C::O_LD + 4 * d4) * 4);
         L += f * x.y;
         a.x += f * v.x, a.y += f * v.y, a.z += f * v.z, a.w += f * v.w;
       }
       if (whole) {
-        const int rr = rb * ROWS + r;
-        if (rr < R && rr % p.N < n) {
+        const int rr = out_rb * ROWS + r;
+        if (rr < R && rr % p.N < out_n) {
           const float inv = L == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / L;
-          reinterpret_cast<uint2*>(p.o)[(row0 + rr) * V4 + d4] =
+          reinterpret_cast<uint2*>(p.o)[(out_row0 + rr) * V4 + d4] =
               make_uint2(pack_16<F16>(a.x * inv, a.y * inv), pack_16<F16>(a.z * inv, a.w * inv));
           if (p.lse != nullptr && d4 == 0)
-            p.lse[row0 + rr] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+            p.lse[out_row0 + rr] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
         }
       } else {
         reinterpret_cast<float4*>(p.part_o)[(static_cast<size_t>(slot) * ROWS + r) * V4 + d4] = a;
         if (d4 == 0) p.part_ml[static_cast<size_t>(slot) * ROWS + r] = make_float2(M, L);
       }
     }
+    if (!more) return;
     __syncthreads();
-    u = item_first + t1;
+    if constexpr (NT > 1) issue_next(NT - 1);
   }
 }
 
