@@ -22,6 +22,7 @@
 #include "fp8_prep_kernel.cuh"
 #include "kv4_attn_kernel.cuh"
 #include "kv4_cache_kernel.cuh"
+#include "kv4_chunk_kernel.cuh"
 #include "mxfp8_quant_kernel.cuh"
 #include "w4a16_kernel.cuh"
 

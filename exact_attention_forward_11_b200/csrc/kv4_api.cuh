@@ -56,26 +56,48 @@ dim3 kv4_move_grid(long long blocks, int sms) {
   return dim3(static_cast<unsigned>(need < cap ? need : cap), 2);
 }
 
-// How attn_fwd_kv4 runs a shape: rows per block, CTAs and workspace (host only; it
-// assumes the SMs of a B200, so that the size does not depend on the current device).
+// How attn_fwd_kv4 runs a shape (host only; it assumes the SMs of a B200, so that the
+// workspace's size does not depend on the current device): by the query rows of one cached head.
 struct Kv4Plan {
-  int nt, row_blocks, ctas;
-  size_t ml_bytes, workspace;
+  int nt;                    // decode kernel: 8-row tiles per block; 0: the chunk kernel
+  int row_blocks, ctas;
+  size_t ml_bytes, o_bytes, workspace;
 };
 constexpr int kKv4Sms = 148;
+#ifndef KV4_CHUNK_ROWS
+#define KV4_CHUNK_ROWS 32
+#endif
 
 Kv4Plan kv4_plan(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {
   Kv4Plan r;
   const long long rows = static_cast<long long>(Hq / Hkv) * N;
-  r.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
-  r.row_blocks = static_cast<int>((rows + 8 * r.nt - 1) / (8 * r.nt));
-  const long long tiles = (static_cast<long long>(max_pages) * page_size + attn::kDecTile - 1) / attn::kDecTile;
+  r.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : (rows <= KV4_CHUNK_ROWS ? 4 : 0));
+  const int block = r.nt > 0 ? 8 * r.nt : attn::kChunkRows, keys = r.nt > 0 ? attn::kDecTile : 128;
+  r.row_blocks = static_cast<int>((rows + block - 1) / block);
+  const long long tiles = (static_cast<long long>(max_pages) * page_size + keys - 1) / keys;
   const long long most = kKv4Sms * (r.nt == 1 ? 2 : 1);
   const double units = static_cast<double>(tiles) * B * Hkv * r.row_blocks;
   r.ctas = static_cast<int>(units < most ? units : most);
-  r.ml_bytes = static_cast<size_t>(2) * r.ctas * 8 * r.nt * sizeof(float2);
-  r.workspace = r.ml_bytes + static_cast<size_t>(2) * r.ctas * 8 * r.nt * d * sizeof(float);
+  r.ml_bytes = static_cast<size_t>(2) * r.ctas * block * sizeof(float2);
+  r.o_bytes = static_cast<size_t>(2) * r.ctas * block * d * sizeof(float);
+  r.workspace = r.ml_bytes + r.o_bytes + (r.nt > 0 ? 0 : (r.ctas * sizeof(attn::Kv4Head) + 15) / 16 * 16);
   return r;
+}
+
+// A kernel that may start while the one before it in the stream runs, and waits for it before it
+// reads what that one wrote.
+template <class P>
+cudaError_t launch_after(void (*kern)(P), dim3 grid, int threads, cudaStream_t stream, const P& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <class C, bool F16>
@@ -83,18 +105,26 @@ attn_status launch_kv4_dec(const attn::Kv4AttnParams& p, int tag, cudaStream_t s
   auto kern = attn::kv4_decode_sm100<C, F16>;
   if (!set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, tag)) return ATTN_ERR_CUDA;
   kern<<<p.ctas, attn::kDecWarps * 32, C::SMEM_BYTES, stream>>>(p);
-  // the join may start (and read lengths) while the main kernel runs; it waits for it before
-  // it reads the workspace
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.c.B * p.Hq * p.N));
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn::kv4_combine_sm100<C, F16>, p);
+  const cudaError_t e = launch_after(attn::kv4_combine_sm100<C, F16>,
+                                     dim3(static_cast<unsigned>(p.c.B * p.Hq * p.N)), 128, stream, p);
+  if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) {
+    forget_smem(tag);
+    return ATTN_ERR_CUDA;
+  }
+  return ATTN_OK;
+}
+
+template <int D, bool F16>
+attn_status launch_kv4_chunk(const attn::Kv4AttnParams& p, const Kv4Plan& plan, int tag, cudaStream_t stream) {
+  using C = attn::Kv4ChunkCfg<D>;
+  auto kern = attn::kv4_chunk_sm100<C, F16>;
+  if (!set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, tag)) return ATTN_ERR_CUDA;
+  attn::Kv4ChunkParams cp;
+  cp.a = p;
+  cp.heads = reinterpret_cast<attn::Kv4Head*>(reinterpret_cast<uint8_t*>(p.part_o) + plan.o_bytes);
+  cp.timeout_cycles = kWaitLimitCycles;
+  kern<<<p.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(cp);
+  const cudaError_t e = launch_after(attn::kv4_chunk_join_sm100<C, F16>, dim3(p.ctas, attn::kChunkRows / 32), 256, stream, cp);
   if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) {
     forget_smem(tag);
     return ATTN_ERR_CUDA;
@@ -104,7 +134,8 @@ attn_status launch_kv4_dec(const attn::Kv4AttnParams& p, int tag, cudaStream_t s
 
 template <int D, bool F16>
 attn_status launch_kv4_rows(const attn::Kv4AttnParams& p, const Kv4Plan& plan, cudaStream_t stream) {
-  const int tag = 16 + (D == 128 ? 0 : 6) + (F16 ? 3 : 0);
+  const int tag = 16 + (D == 128 ? 0 : 8) + (F16 ? 4 : 0);
+  if (plan.nt == 0) return launch_kv4_chunk<D, F16>(p, plan, tag + 3, stream);
   if (plan.nt == 1) return launch_kv4_dec<attn::Kv4DecCfg<D, 1>, F16>(p, tag, stream);
   if (plan.nt == 2) return launch_kv4_dec<attn::Kv4DecCfg<D, 2>, F16>(p, tag + 1, stream);
   return launch_kv4_dec<attn::Kv4DecCfg<D, 4>, F16>(p, tag + 2, stream);

@@ -1,0 +1,628 @@
+// kv4_chunk_kernel.cuh - attention over the 4-bit cache for many query rows per cached head
+// (include/kv4_b200.h): chunks of prompts, where the tensor cores bound.
+//
+// The G = Hq / Hkv query heads times N query tokens of one (sequence b, cached head h) are R = G N
+// rows over the same keys; a unit is 256 of them, two 128-row tiles that share every converted
+// key tile, so a cached value is converted once per 256 rows. On-chip schedule of
+// attn_fwd_kernel.cuh (S_t = Q_t K^T and O_t += P_t V on tcgen05 with S, P and O in tensor
+// memory, one softmax thread per row, a lazily moved maximum), with these differences:
+//  * K^ and V^ do not come by TMA: warps 8-11 read the codes of the next 128-key tile into
+//    registers (a thread owns one key row: page lookups two tiles ahead, codes one tile ahead),
+//    turn them into f16 (one conversion per two codes and one multiplication by the block scale,
+//    both exact) and store them in the 128-byte-swizzled layout that the MMA reads, K^ and V^
+//    double-buffered. Keys behind the sequence's end are stored as zeros.
+//  * q rows are scaled by a power of two and rounded to f16 by their own softmax threads (the
+//    bf16 q would need bf16 K^; f16 holds every cached value and gives P three more bits).
+//  * The 128-key tiles of all units make one list that is cut into equal runs, one per CTA, as in
+//    kv4_attn_kernel.cuh (causal units count only the tiles that their rows see): 148 CTAs of
+//    equal work whatever the lengths. A unit that several runs share is joined by
+//    kv4_chunk_join_sm100 from fp32 parts in the workspace, in the order of the runs.
+//
+// CTA: 16 warps. 0-3 softmax of tile 0, 4-7 of tile 1, 8-11 conversion, 12 MMA issuer (owns
+// TMEM), 13-15 idle. TMEM and MMA order: attn_fwd_kernel.cuh.
+// Bound: 4 * 128 * 128 * D operations of a (tile, 128 keys) take 1024 clocks of the tensor pipe at
+// D = 128, its 16384 exponentials 1024 clocks of the MUFU units.
+#pragma once
+
+#include "attn_fwd_kernel.cuh"
+#include "kv4_attn_kernel.cuh"
+
+namespace attn {
+
+template <int D_>
+struct Kv4ChunkCfg {
+  static constexpr int D = D_;
+  static constexpr int CHUNKS = D / 64;                         // 128-byte column chunks of a row of f16
+  static constexpr int CHUNK_BYTES = 128 * 128;
+  static constexpr int TILE_BYTES = CHUNKS * CHUNK_BYTES;       // 128 rows of f16
+  static constexpr int CODE_ROW = D / 2, SF_ROW = D / 16;
+  static constexpr int S_KSTEPS = D / 16, PV_KSTEPS = 8;
+  static constexpr int P_CHUNKS = 2;                            // (as p_row_to_tmem writes them)
+  static constexpr bool PV_F16 = true;
+  static constexpr int THREADS = 512;
+  static constexpr int CONV_WARP = 8, MMA_WARP = 12;
+  // launch: 65536 / 512 = 128 registers a thread; 2 * 128 * 184 + 128 * 88 + 128 * 56 = 65536
+  static constexpr uint32_t REGS_SOFTMAX = 184, REGS_CONV = 88, REGS_MMA = 56;
+  static_assert(2 * REGS_SOFTMAX + REGS_CONV + REGS_MMA <= 512, "register split");
+  static constexpr uint32_t TMEM_COLS = 512, O_COL0 = 256;
+  static constexpr float RESCALE_THRESHOLD = 8.0f;
+  static constexpr int SMEM_Q = 0;                              // 2 tiles
+  static constexpr int SMEM_K = 2 * TILE_BYTES;                 // 2 buffers
+  static constexpr int SMEM_V = 4 * TILE_BYTES;                 // 2 buffers
+  static constexpr int SMEM_BAR = 6 * TILE_BYTES;
+  // q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_done[2], drain
+  static constexpr int NUM_BARS = 2 * 7 + 4 + 1;
+  static constexpr int SMEM_MISC = SMEM_BAR + NUM_BARS * 8;
+  static constexpr int SMEM_BYTES = SMEM_MISC + 16 + 1024;
+};
+constexpr int kChunkRows = 256;
+template <int D>
+struct SfWords { static constexpr int N = D / 64; };   // 32-bit words of a row's scale bytes
+
+// A unit's first part, as the CTA that wrote it leaves it for the join.
+struct Kv4Head {
+  int parts;                 // 0: this CTA has none
+  int b, h, qp, slot;
+};
+
+struct Kv4ChunkParams {
+  Kv4AttnParams a;           // part_o: [2 ctas][256][D], part_ml: [2 ctas][256]; row_blocks = ceil(R / 256)
+  Kv4Head* heads;            // [ctas]
+  uint64_t timeout_cycles;
+};
+
+// Key tiles that the 128 rows from r0 of sequence (len, n) see, and (through `all`) the last key
+// that every valid row among them sees.
+__device__ __forceinline__ int kv4_row_tiles(const Kv4AttnParams& p, int len, int n, int r0, int R, int& all) {
+  all = len - 1;
+  if (r0 >= R || n == 0) return 0;
+  const int span = min(128, R - r0), i0 = r0 % p.N;
+  const bool wraps = i0 + span > p.N;                // the rows reach into the next head
+  if (i0 >= n && !wraps) return 0;
+  if (!p.causal) return (len + 127) >> 7;
+  const int most = i0 < n ? (wraps ? n - 1 : min(n - 1, i0 + span - 1)) : min(n - 1, i0 + span - p.N - 1);
+  all = len - n + (wraps ? 0 : i0);
+  return (max(0, min(len, len - n + most + 1)) + 127) >> 7;
+}
+
+// Walks a run's segments: tiles [kt0, kt1) of unit (b, qp, h), its two row tiles seeing keys up to
+// tile end[t]. Units are ordered by sequence, row pair, head.
+struct Kv4ChunkWalk {
+  const Kv4AttnParams& p;
+  int R;
+  long long u, u_end, first;                         // first: first tile of (b, qp)
+  int b, qp, h, len, n, kt0, kt1, nkv, lim_all;
+  int end[2];
+
+  __device__ __forceinline__ explicit Kv4ChunkWalk(const Kv4AttnParams& params)
+      : p(params), R(params.Hq / params.c.H * params.N) {}
+
+  // tiles of one head of (b, qp) = idx
+  __device__ __forceinline__ int tiles(int idx) {
+    const int bb = idx / p.row_blocks, q = idx - bb * p.row_blocks;
+    const int l = kv4_len(p.c, bb), nn = kv4_qlen(p, bb);
+    int all;
+    return max(kv4_row_tiles(p, l, nn, q * kChunkRows, R, all), kv4_row_tiles(p, l, nn, q * kChunkRows + 128, R, all));
+  }
+  // total tiles (the whole warp takes part)
+  __device__ __forceinline__ long long total(int lane) {
+    long long s = 0;
+    for (int i = lane; i < p.c.B * p.row_blocks; i += 32) s += tiles(i);
+    return warp_sum(s) * p.c.H;
+  }
+  // to the run [u0, u1) (the whole warp takes part)
+  __device__ __forceinline__ void seek(long long u0, long long u1, int lane) {
+    u = u0;
+    u_end = u1;
+    first = 0;
+    for (int i0 = 0;; i0 += 32) {
+      const long long mine = i0 + lane < p.c.B * p.row_blocks ? static_cast<long long>(tiles(i0 + lane)) * p.c.H : 0;
+      long long incl = mine;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += o;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, first + incl > u);
+      if (hit != 0u) {
+        const int l = __ffs(hit) - 1;
+        b = (i0 + l) / p.row_blocks;
+        qp = (i0 + l) % p.row_blocks;
+        first += __shfl_sync(0xffffffffu, incl - mine, l);
+        break;
+      }
+      first += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  // the segment that starts at u (u < u_end); moves u behind it
+  __device__ __forceinline__ void next() {
+    int a0, a1;
+    for (;;) {
+      len = kv4_len(p.c, b);
+      n = kv4_qlen(p, b);
+      end[0] = kv4_row_tiles(p, len, n, qp * kChunkRows, R, a0);
+      end[1] = kv4_row_tiles(p, len, n, qp * kChunkRows + 128, R, a1);
+      nkv = max(end[0], end[1]);
+      if (u < first + static_cast<long long>(nkv) * p.c.H) break;
+      first += static_cast<long long>(nkv) * p.c.H;
+      if (++qp == p.row_blocks) qp = 0, ++b;
+    }
+    lim_all = min(end[0] > 0 ? a0 : len - 1, end[1] > 0 ? a1 : len - 1);
+    const uint32_t off = static_cast<uint32_t>(u - first);
+    h = static_cast<int>(off / static_cast<uint32_t>(nkv));
+    kt0 = static_cast<int>(off - static_cast<uint32_t>(h) * nkv);
+    kt1 = static_cast<int>(min(static_cast<long long>(nkv), kt0 + (u_end - u)));
+    u += kt1 - kt0;
+    end[0] = min(end[0], kt1);
+    end[1] = min(end[1], kt1);
+  }
+  __device__ __forceinline__ bool whole() const { return kt0 == 0 && kt1 == nkv; }
+};
+
+// O = 0, LSE = -infinity for the rows that see no key.
+template <int D>
+__device__ __forceinline__ void kv4_empty_rows(const Kv4AttnParams& p, int threads) {
+  for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
+    const int len = kv4_len(p.c, b), n = kv4_qlen(p, b);
+    const int z = len == 0 ? n : (p.causal ? max(0, n - len) : 0);
+    if (z == 0) continue;
+    constexpr int V4 = D / 8;                        // 16-byte pieces of a row
+    for (long long i = threadIdx.x; i < static_cast<long long>(p.Hq) * z * V4; i += threads) {
+      const long long r = i / V4;
+      const size_t row = (static_cast<size_t>(b) * p.Hq + r / z) * p.N + r % z;
+      reinterpret_cast<uint4*>(p.o)[row * V4 + i % V4] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse != nullptr && i % V4 == 0) p.lse[row] = -INFINITY;
+    }
+  }
+}
+
+template <class C, bool F16>
+__global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkParams cp) {
+  using namespace b200;
+  constexpr int D = C::D;
+  const Kv4AttnParams& p = cp.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::SMEM_BAR);
+  uint64_t* k_full = q_full + 2;
+  uint64_t* k_empty = k_full + 2;
+  uint64_t* v_full = k_empty + 2;
+  uint64_t* v_empty = v_full + 2;
+  uint64_t* s_full = v_empty + 2;
+  uint64_t* p_full = s_full + 2;                     // [tile][chunk]
+  uint64_t* o_done = p_full + 4;
+  uint64_t* drain_bar = o_done + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC);
+  uint32_t* abort_word = tmem_slot + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 128);
+      mbar_init(k_full + i, 4);
+      mbar_init(k_empty + i, 1);
+      mbar_init(v_full + i, 4);
+      mbar_init(v_empty + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + 2 * i, 128);
+      mbar_init(p_full + 2 * i + 1, 128);
+      mbar_init(o_done + i, 1);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_word = 0u;
+    fence_barrier_init();
+    fence_proxy_async_shared();
+    cp.heads[blockIdx.x].parts = 0;
+  }
+  if (warp == C::MMA_WARP) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  kv4_empty_rows<D>(p, C::THREADS);
+  Kv4ChunkWalk w(p);
+  const Kv4Runs runs(w.total(lane), p.ctas);
+  const bool idle = static_cast<int>(blockIdx.x) >= runs.n;
+  const long long u0 = idle ? 0 : runs.start(blockIdx.x), u1 = idle ? 0 : runs.start(blockIdx.x + 1);
+  if (!idle) w.seek(u0, u1, lane);
+  w.u = u0;
+  w.u_end = u1;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const Waiter waiter{abort_word, cp.timeout_cycles};
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, waiter.wait(bar, parity)); };
+  bool ok = true;
+
+  if (warp >= C::MMA_WARP) {
+    // ======================= MMA issuer =======================
+    regs_decrease<C::REGS_MMA>();
+    if (warp == C::MMA_WARP) {
+      const uint32_t leader = elect_one() ? 1u : 0u;
+      auto commit = [&](uint64_t* bar) { mma_commit(bar, leader); };
+      constexpr uint32_t idesc_s = instr_desc(0u, 128, 128, 0, 0);
+      constexpr uint32_t idesc_o = instr_desc(0u, 128, D, 0, 1);
+      constexpr uint32_t hi = smem_desc_hi(1024);
+      const uint32_t q_lo = smem_desc_lo(smem_addr(smem + C::SMEM_Q), 16);
+      const uint32_t k_lo = smem_desc_lo(smem_addr(smem + C::SMEM_K), 16);
+      const uint32_t v_lo = smem_desc_lo(smem_addr(smem + C::SMEM_V), C::CHUNK_BYTES);
+      auto issue_s = [&](int t, uint32_t buf) {
+        const uint32_t qa = q_lo + ((t * C::TILE_BYTES) >> 4), ka = k_lo + ((buf * C::TILE_BYTES) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < C::S_KSTEPS; ++kk) {
+          const uint32_t off = ((kk / 4) * C::CHUNK_BYTES + (kk % 4) * 32) >> 4;
+          mma_f16_ss(tmem_base + t * 128, smem_desc(qa + off, hi), smem_desc(ka + off, hi), idesc_s, kk > 0, leader);
+        }
+      };
+      auto issue_pv = [&](int t, uint32_t buf, int c, bool acc) {
+        const uint32_t va = v_lo + ((buf * C::TILE_BYTES) >> 4);
+#pragma unroll
+        for (int i = 0; i < C::PV_KSTEPS / 2; ++i) {
+          const int kv = c * (C::PV_KSTEPS / 2) + i;
+          mma_f16_ts(tmem_base + C::O_COL0 + t * D, tmem_base + t * 128 + kv * 8, smem_desc(va + ((kv * 16 * 128) >> 4), hi),
+                     idesc_o, (acc || i > 0) ? 1u : 0u, leader);
+        }
+      };
+      uint32_t k = 0;                                // key tiles used so far
+      uint32_t qc = 0, pc = 0;                       // phases of q_full and p_full: bit t
+      while (ok && w.u < w.u_end) {
+        w.next();
+        // S of the segment's first tile (issued after the previous segment's last P V on this
+        // thread, so it overwrites that P only after it has been read)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (w.end[t] > w.kt0) {
+            if (!(ok = wait_all(q_full + t, (qc >> t) & 1u))) break;
+            qc ^= 1u << t;
+          }
+        if (!ok || !(ok = wait_all(k_full + (k & 1), (k >> 1) & 1))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (w.end[t] > w.kt0) {
+            issue_s(t, k & 1);
+            commit(s_full + t);
+          }
+        commit(k_empty + (k & 1));
+        for (int j = w.kt0; j < w.kt1; ++j, ++k) {
+          const uint32_t k1 = k + 1;
+          if (!(ok = wait_all(v_full + (k & 1), (k >> 1) & 1))) break;
+          bool k_ready = false;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (j >= w.end[t]) continue;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (!(ok = wait_all(p_full + 2 * t + c, (pc >> t) & 1u))) break;
+              tc_fence_after();
+              issue_pv(t, k & 1, c, j > w.kt0 || c > 0);
+            }
+            if (!ok) break;
+            pc ^= 1u << t;
+            if (j + 1 < w.end[t]) {
+              if (!k_ready) {
+                if (!(ok = wait_all(k_full + (k1 & 1), (k1 >> 1) & 1))) break;
+                k_ready = true;
+                tc_fence_after();
+              }
+              issue_s(t, k1 & 1);
+              commit(s_full + t);
+            } else {
+              commit(o_done + t);
+            }
+          }
+          if (!ok) break;
+          commit(v_empty + (k & 1));
+          if (k_ready) commit(k_empty + (k1 & 1));
+        }
+      }
+      if (!ok && lane == 0) record_timeout();
+      // every MMA this warp issued completes before TMEM can be released
+      commit(drain_bar);
+      drain_wait(drain_bar, 0, cp.timeout_cycles);
+      __syncwarp();
+    }
+  } else if (warp >= C::CONV_WARP) {
+    // ======================= codes -> f16 K^ and V^ =======================
+    regs_decrease<C::REGS_CONV>();
+    const int kr = threadIdx.x - C::CONV_WARP * 32;   // key row of this thread
+    constexpr int NW = C::CODE_ROW / 16;              // 16-byte pieces of a row's codes
+    const uint32_t slot_mask = (1u << p.c.page_shift) - 1u;
+    const long long tiles = u1 - u0;
+    // the load position: tile lj of the walk's segment
+    int lj = 0;
+    auto step = [&]() {                               // to the next tile (the first at the first call)
+      if (w.u > u0 && lj + 1 < w.kt1) {
+        ++lj;
+      } else if (w.u < w.u_end) {
+        w.next();
+        lj = w.kt0;
+      }
+    };
+    auto page_of = [&]() {                            // page of this thread's key; what lies behind the end: none
+      const int key = lj * 128 + kr;
+      return key < w.len ? p.c.block_table[static_cast<long long>(w.b) * p.c.max_pages + (key >> p.c.page_shift)] : -1;
+    };
+    uint4 kw[NW], vw[NW];
+    uint32_t ksf[SfWords<D>::N], vsf_next[SfWords<D>::N], vsf[SfWords<D>::N];
+    uint32_t row = 0;
+    bool valid = false, edge = false;                 // the key exists; some row does not see it
+    // the row of the tile at the load position (its page has been looked up), and K's codes, with the
+    // scales of both
+    auto load_k = [&](int page) {
+      const int key = lj * 128 + kr;
+      valid = key < w.len && kv4_row(p.c, page, w.h, key & static_cast<int>(slot_mask), row);
+      edge = key > w.lim_all;
+#pragma unroll
+      for (int i = 0; i < SfWords<D>::N; ++i) ksf[i] = vsf_next[i] = 0u;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) kw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (valid) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.c.codes[0] + static_cast<size_t>(row) * C::CODE_ROW);
+#pragma unroll
+        for (int i = 0; i < NW; ++i) kw[i] = __ldg(src + i);
+#pragma unroll
+        for (int i = 0; i < SfWords<D>::N; ++i) {
+          ksf[i] = __ldg(reinterpret_cast<const uint32_t*>(p.c.sf[0] + static_cast<size_t>(row) * C::SF_ROW) + i);
+          vsf_next[i] = __ldg(reinterpret_cast<const uint32_t*>(p.c.sf[1] + static_cast<size_t>(row) * C::SF_ROW) + i);
+        }
+      }
+    };
+    auto load_v = [&]() {
+#pragma unroll
+      for (int i = 0; i < NW; ++i) vw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (valid) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.c.codes[1] + static_cast<size_t>(row) * C::CODE_ROW);
+#pragma unroll
+        for (int i = 0; i < NW; ++i) vw[i] = __ldg(src + i);
+      }
+    };
+    // a row of D f16 values, written to row kr of the tile at dst
+    auto convert = [&](const uint4 (&cw)[NW], const uint32_t (&sf)[SfWords<D>::N], uint8_t* dst) {
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {                  // 32 values, two blocks
+        const uint32_t s2 = f16x2_from_e4m3x2(static_cast<uint16_t>(sf[i >> 1] >> (16 * (i & 1))));
+        const uint32_t wds[4] = {cw[i].x, cw[i].y, cw[i].z, cw[i].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {                 // 8 values: one 16-byte unit of the f16 row
+          uint32_t f[4];
+          f16x2_from_e2m1x8(wds[q], f);
+          const uint32_t sc = q < 2 ? splat_lo(s2) : splat_hi(s2);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = hmul2(f[e], sc);
+          const int un = 4 * i + q;
+          *reinterpret_cast<uint4*>(dst + (un >> 3) * C::CHUNK_BYTES + kr * 128 + (((un & 7) ^ (kr & 7)) << 4)) =
+              make_uint4(f[0], f[1], f[2], f[3]);
+        }
+      }
+    };
+    int page = -1;
+    if (tiles > 0) {
+      step();
+      load_k(page_of());
+      load_v();
+    }
+    for (long long k = 0; ok && k < tiles; ++k) {
+      const uint32_t buf = static_cast<uint32_t>(k) & 1u, round = static_cast<uint32_t>(k >> 1);
+#pragma unroll
+      for (int i = 0; i < SfWords<D>::N; ++i) vsf[i] = vsf_next[i];
+      // A NaN value must reach the rows that see it and no other, and P = 0 would not keep it from a
+      // masked row: where some row does not see the key, its value counts as zero and its key becomes
+      // NaN, so that it arrives through the scores.
+      if (edge) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < SfWords<D>::N; ++i) bad = bad || any_nan_scale(vsf[i]);
+        if (bad) {
+#pragma unroll
+          for (int i = 0; i < SfWords<D>::N; ++i) ksf[i] = 0x7F7F7F7Fu, vsf[i] = 0u;
+        }
+      }
+      const bool more = k + 1 < tiles;
+      if (more) {
+        step();
+        page = page_of();
+      }
+      if (k >= 2 && !(ok = wait_all(k_empty + buf, (round - 1) & 1))) break;
+      convert(kw, ksf, smem + C::SMEM_K + buf * C::TILE_BYTES);
+      fence_proxy_async_shared();   // the MMA (async proxy) reads what these threads wrote
+      __syncwarp();
+      if (lane == 0) mbar_arrive(k_full + buf);
+      if (more) load_k(page);
+      if (k >= 2 && !(ok = wait_all(v_empty + buf, (round - 1) & 1))) break;
+      convert(vw, vsf, smem + C::SMEM_V + buf * C::TILE_BYTES);
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_full + buf);
+      if (more) load_v();
+    }
+    if (!ok && lane == 0) record_timeout();
+  } else {
+    // ======================= softmax: one thread per row =======================
+    regs_increase<C::REGS_SOFTMAX>();
+    const int t = warp >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;                     // row inside the tile
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t s_tm = tmem_base + lane_off + t * 128;
+    const uint32_t o_tm = tmem_base + lane_off + C::O_COL0 + t * D;
+    uint32_t sc = 0, oc = 0;                          // phases of s_full and o_done
+    while (ok && w.u < w.u_end) {
+      const bool first_segment = w.u == u0;
+      w.next();
+      const bool whole = w.whole();
+      const int rr = w.qp * kChunkRows + t * 128 + r; // row of (b, h)
+      const int slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
+      const int i_tok = rr % p.N;
+      const size_t row = (static_cast<size_t>(w.b) * p.c.H + w.h) * w.R + rr;
+      const size_t prow = static_cast<size_t>(slot) * kChunkRows + t * 128 + r;
+      if (w.kt0 == 0 && !whole && threadIdx.x == 0) { // the unit's first part: what the join needs
+        const long long unit0 = w.u - w.kt1;
+        Kv4Head hd;
+        hd.parts = runs.cta_of(unit0 + w.nkv - 1) - static_cast<int>(blockIdx.x) + 1;
+        hd.b = w.b, hd.h = w.h, hd.qp = w.qp, hd.slot = slot;
+        cp.heads[blockIdx.x] = hd;
+      }
+      const int endt = t == 0 ? w.end[0] : w.end[1];
+      if (endt <= w.kt0) {
+        if (!whole) p.part_ml[prow] = make_float2(-INFINITY, 0.f);
+        continue;
+      }
+      // ---- the row's q: scaled by a power of two, f16, into the tile's swizzled rows. Every S
+      // MMA that read the previous q has completed: this thread saw the last one's barrier.
+      float c;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D * 2);
+        float amax = 0.f;
+        const bool have = rr < w.R;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = have ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = f32x2_from_16<F16>(xs[e]);
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+        const int e2 = kv4_row_exp(amax);
+        const float down = __int_as_float((254 - e2) << 23);
+        c = fmaxf(__int_as_float(e2 << 23) * p.scale_log2, 1e-37f);
+        uint8_t* qrow = smem + C::SMEM_Q + t * C::TILE_BYTES + r * 128;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = have ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+          uint32_t y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = f32x2_from_16<F16>(xs[e]);
+            y[e] = pack_f16x2(f.x * down, f.y * down);
+          }
+          *reinterpret_cast<uint4*>(qrow + (i >> 3) * C::CHUNK_BYTES + (((i & 7) ^ (r & 7)) << 4)) =
+              make_uint4(y[0], y[1], y[2], y[3]);
+        }
+        fence_proxy_async_shared();
+        mbar_arrive(q_full + t);
+      }
+      // last key this row sees (rows that hold no query see everything: they are not written)
+      const int lim = p.causal && i_tok < w.n ? w.len - w.n + i_tok : w.len - 1;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = w.kt0; j < endt; ++j) {
+        if (!(ok = wait_all(s_full + t, sc & 1))) break;
+        ++sc;
+        tc_fence_after();
+        uint32_t sr[128];
+        tmem_ld32(s_tm + 0, sr + 0);
+        tmem_ld32(s_tm + 32, sr + 32);
+        tmem_ld32(s_tm + 64, sr + 64);
+        tmem_ld32(s_tm + 96, sr + 96);
+        tmem_ld_wait<128>(sr);
+        const int limit = lim - j * 128;
+        if (__any_sync(0xffffffffu, limit < 127)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i > limit) sr[i] = 0xff800000u;       // -inf
+        }
+        const float m_blk = row_max128(sr) * c;
+        float m_use = m_run;
+        if (m_blk - m_run > C::RESCALE_THRESHOLD) m_use = m_blk;
+        const bool moved = m_use != m_run;
+        const float alpha = moved ? ex2_approx(m_run - m_use) : 1.f;
+        if (j > w.kt0 && __any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int cb = 0; cb < D; cb += 32) {
+            uint32_t ov[32];
+            tmem_ld32(o_tm + cb, ov);
+            tmem_ld_wait<32>(ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st32(o_tm + cb, ov);
+          }
+        }
+        // (a row that has seen no key yet: every score is -infinity, every P 0)
+        const float sum = p_row_to_tmem<C, 0u>(sr, c, m_use == -INFINITY ? 0.f : m_use, s_tm, p_full + 2 * t);
+        l_run = l_run * alpha + sum;
+        m_run = m_use;
+      }
+      if (!ok) break;
+      if (!(ok = wait_all(o_done + t, oc & 1))) break;
+      ++oc;
+      tc_fence_after();
+      const float f = whole ? (l_run == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / l_run) : 1.f;
+      const bool write = whole ? rr < w.R && i_tok < w.n : true;
+#pragma unroll
+      for (int cb = 0; cb < D; cb += 32) {
+        uint32_t ov[32];
+        tmem_ld32(o_tm + cb, ov);
+        tmem_ld_wait<32>(ov);
+        if (whole) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            pk[i] = pack_16<F16>(__uint_as_float(ov[2 * i]) * f, __uint_as_float(ov[2 * i + 1]) * f);
+          if (write) {
+            uint4* dst = reinterpret_cast<uint4*>(p.o + (row * D + cb) * 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + cb);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+        }
+      }
+      if (!whole) p.part_ml[prow] = make_float2(m_run, l_run);
+      else if (p.lse != nullptr && write)
+        p.lse[row] = l_run == 0.f ? -INFINITY : (m_run + __log2f(l_run)) * 0.69314718055994531f;
+    }
+    if (!ok) record_timeout();
+  }
+
+  // ---- teardown: every TMEM access and MMA of this CTA is complete here
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == C::MMA_WARP) tmem_dealloc(tmem_base, C::TMEM_COLS);
+}
+
+// Joins the parts of the unit whose first part CTA blockIdx.x wrote: 32 rows per block of 256
+// threads, a warp per row at a time, D / 32 channels a lane.
+template <class C, bool F16>
+__global__ void __launch_bounds__(256) kv4_chunk_join_sm100(const Kv4ChunkParams cp) {
+  constexpr int D = C::D, E = D / 32;
+  const Kv4AttnParams& p = cp.a;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Kv4Head hd = cp.heads[blockIdx.x];
+  if (hd.parts == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int R = p.Hq / p.c.H * p.N, n = kv4_qlen(p, hd.b);
+  for (int k = warp; k < 32; k += 8) {
+    const int r = blockIdx.y * 32 + k, rr = hd.qp * kChunkRows + r;
+    if (rr >= R || rr % p.N >= n) continue;
+    float M = -INFINITY, L = 0.f, a[E] = {};
+#pragma unroll 4
+    for (int i = 0; i < hd.parts; ++i) {
+      const size_t at = static_cast<size_t>(i == 0 ? hd.slot : 2 * (static_cast<int>(blockIdx.x) + i)) * kChunkRows + r;
+      const float2 x = __ldcg(p.part_ml + at);
+      if (x.x == -INFINITY && x.y == 0.f) continue;   // the part's keys lie behind this row's (nothing written)
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = __ldcg(p.part_o + at * D + lane + 32 * e);
+      const float Mn = fmaxf(M, x.x), Mu = Mn == -INFINITY ? 0.f : Mn;
+      const float fo = b200::ex2_approx(M - Mu), fn = b200::ex2_approx(x.x - Mu);
+      L = L * fo + x.y * fn;
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] = a[e] * fo + v[e] * fn;
+      M = Mn;
+    }
+    const float inv = L == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / L;
+    const size_t row = (static_cast<size_t>(hd.b) * p.c.H + hd.h) * R + rr;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      reinterpret_cast<uint16_t*>(p.o)[row * D + lane + 32 * e] = static_cast<uint16_t>(pack_16<F16>(a[e] * inv, 0.f));
+    if (p.lse != nullptr && lane == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+  }
+}
+
+}  // namespace attn
