@@ -7,8 +7,7 @@
 // attn_fwd_kernel.cuh (S_t = Q_t K^T and O_t += P_t V on tcgen05 with S, P and O in tensor
 // memory, one softmax thread per row, a lazily moved maximum), with these differences:
 //  * K^ and V^ do not come by TMA: warps 8-11 read the codes of the next 128-key tile into
-//    registers (a thread owns one key row: page lookups two tiles ahead, codes one tile ahead),
-//    turn them into f16 (one conversion per two codes and one multiplication by the block scale,
+//    registers (a thread owns one key row), turn them into f16 (one conversion per two codes and one multiplication by the block scale,
 //    both exact) and store them in the 128-byte-swizzled layout that the MMA reads, K^ and V^
 //    double-buffered. Keys behind the sequence's end are stored as zeros.
 //  * q rows are scaled by a power of two and rounded to f16 by their own softmax threads (the
@@ -19,7 +18,11 @@
 //    kv4_chunk_join_sm100 from fp32 parts in the workspace, in the order of the runs.
 //
 // CTA: 16 warps. 0-3 softmax of tile 0, 4-7 of tile 1, 8-11 conversion, 12 MMA issuer (owns
-// TMEM), 13-15 idle. TMEM and MMA order: attn_fwd_kernel.cuh.
+// TMEM), 13 walks the run: it hands out the segments (a unit's tiles [kt0, kt1)) and, tile by
+// tile, the cache row of every key through small rings in shared memory, so that neither the page
+// lookups nor the walk's state burden the other warps (with every warp walking for itself the
+// conversion and softmax warps spilled: 1.31 against 1.06 ms on 2048 queries x 32 heads over 32768
+// keys); 14-15 write the rows that see no key. TMEM and MMA order: attn_fwd_kernel.cuh.
 // Bound: 4 * 128 * 128 * D operations of a (tile, 128 keys) take 1024 clocks of the tensor pipe at
 // D = 128, its 16384 exponentials 1024 clocks of the MUFU units.
 #pragma once
@@ -40,7 +43,7 @@ struct Kv4ChunkCfg {
   static constexpr int P_CHUNKS = 2;                            // (as p_row_to_tmem writes them)
   static constexpr bool PV_F16 = true;
   static constexpr int THREADS = 512;
-  static constexpr int CONV_WARP = 8, MMA_WARP = 12;
+  static constexpr int CONV_WARP = 8, MMA_WARP = 12, WALK_WARP = 13;
   // launch: 65536 / 512 = 128 registers a thread; 2 * 128 * 184 + 128 * 88 + 128 * 56 = 65536
   static constexpr uint32_t REGS_SOFTMAX = 184, REGS_CONV = 88, REGS_MMA = 56;
   static_assert(2 * REGS_SOFTMAX + REGS_CONV + REGS_MMA <= 512, "register split");
@@ -50,12 +53,28 @@ struct Kv4ChunkCfg {
   static constexpr int SMEM_K = 2 * TILE_BYTES;                 // 2 buffers
   static constexpr int SMEM_V = 4 * TILE_BYTES;                 // 2 buffers
   static constexpr int SMEM_BAR = 6 * TILE_BYTES;
-  // q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_done[2], drain
-  static constexpr int NUM_BARS = 2 * 7 + 4 + 1;
-  static constexpr int SMEM_MISC = SMEM_BAR + NUM_BARS * 8;
-  static constexpr int SMEM_BYTES = SMEM_MISC + 16 + 1024;
+  static constexpr int RING = 4;                                // segments, and tiles, handed out ahead
+  // q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_done[2], drain,
+  // seg_full[RING], seg_empty[RING], row_full[RING], row_empty[RING]
+  static constexpr int NUM_BARS = 2 * 7 + 4 + 1 + 4 * RING;
+  static constexpr int SMEM_MISC = SMEM_BAR + (NUM_BARS + 1) / 2 * 16;
+  static constexpr int SMEM_SEG = SMEM_MISC + 16;               // Kv4Seg[RING]
+  static constexpr int SMEM_ROWS = SMEM_SEG + RING * 64;        // [RING][128] cache rows, [RING] first edge key
+  static constexpr int SMEM_BYTES = SMEM_ROWS + RING * (128 + 4) * 4 + 1024;
 };
 constexpr int kChunkRows = 256;
+
+// A segment as the walking warp hands it out.
+struct __align__(16) Kv4Seg {
+  int kt0, kt1;              // its key tiles (kt0 == kt1: the run is over)
+  int end[2];                // the row tiles see keys up to these tiles (at most kt1)
+  int len, n;                // of the sequence
+  int r0, slot;              // first row of the unit in (b, h); part slot, or -1 for a whole unit
+  unsigned long long row;    // row of (b, h, 0) in q and o
+};
+static_assert(sizeof(Kv4Seg) <= 64, "segment ring");
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;       // a key behind the end
+constexpr int kNoTile = static_cast<int>(0x80000000u);
 template <int D>
 struct SfWords { static constexpr int N = D / 64; };   // 32-bit words of a row's scale bytes
 
@@ -161,13 +180,13 @@ struct Kv4ChunkWalk {
 
 // O = 0, LSE = -infinity for the rows that see no key.
 template <int D>
-__device__ __forceinline__ void kv4_empty_rows(const Kv4AttnParams& p, int threads) {
+__device__ __forceinline__ void kv4_empty_rows(const Kv4AttnParams& p, int thread, int threads) {
   for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
     const int len = kv4_len(p.c, b), n = kv4_qlen(p, b);
     const int z = len == 0 ? n : (p.causal ? max(0, n - len) : 0);
     if (z == 0) continue;
     constexpr int V4 = D / 8;                        // 16-byte pieces of a row
-    for (long long i = threadIdx.x; i < static_cast<long long>(p.Hq) * z * V4; i += threads) {
+    for (long long i = thread; i < static_cast<long long>(p.Hq) * z * V4; i += threads) {
       const long long r = i / V4;
       const size_t row = (static_cast<size_t>(b) * p.Hq + r / z) * p.N + r % z;
       reinterpret_cast<uint4*>(p.o)[row * V4 + i % V4] = make_uint4(0u, 0u, 0u, 0u);
@@ -192,8 +211,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
   uint64_t* p_full = s_full + 2;                     // [tile][chunk]
   uint64_t* o_done = p_full + 4;
   uint64_t* drain_bar = o_done + 2;
+  uint64_t* seg_full = drain_bar + 1;
+  uint64_t* seg_empty = seg_full + C::RING;
+  uint64_t* row_full = seg_empty + C::RING;
+  uint64_t* row_empty = row_full + C::RING;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC);
   uint32_t* abort_word = tmem_slot + 1;
+  Kv4Seg* segs = reinterpret_cast<Kv4Seg*>(smem + C::SMEM_SEG);
+  static_assert(sizeof(Kv4Seg) * C::RING <= C::SMEM_ROWS - C::SMEM_SEG, "segment ring");
+  uint32_t* rows = reinterpret_cast<uint32_t*>(smem + C::SMEM_ROWS);      // [RING][128]
+  int* edges = reinterpret_cast<int*>(rows + C::RING * 128);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;");
 
@@ -210,23 +237,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
       mbar_init(o_done + i, 1);
     }
     mbar_init(drain_bar, 1);
+    for (int i = 0; i < C::RING; ++i) {
+      mbar_init(seg_full + i, 1);
+      mbar_init(seg_empty + i, 9);                   // eight softmax warps, the MMA warp
+      mbar_init(row_full + i, 1);
+      mbar_init(row_empty + i, 4);                   // conversion warps
+    }
     *abort_word = 0u;
     fence_barrier_init();
     fence_proxy_async_shared();
-    cp.heads[blockIdx.x].parts = 0;
   }
   if (warp == C::MMA_WARP) {
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
-  kv4_empty_rows<D>(p, C::THREADS);
-  Kv4ChunkWalk w(p);
-  const Kv4Runs runs(w.total(lane), p.ctas);
-  const bool idle = static_cast<int>(blockIdx.x) >= runs.n;
-  const long long u0 = idle ? 0 : runs.start(blockIdx.x), u1 = idle ? 0 : runs.start(blockIdx.x + 1);
-  if (!idle) w.seek(u0, u1, lane);
-  w.u = u0;
-  w.u_end = u1;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -234,6 +258,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
   const Waiter waiter{abort_word, cp.timeout_cycles};
   auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, waiter.wait(bar, parity)); };
   bool ok = true;
+  // segment number sg of the run: waits for it, and gives it back
+  auto take_segment = [&](uint32_t sg) { return wait_all(seg_full + sg % C::RING, (sg / C::RING) & 1u); };
+  auto free_segment = [&](uint32_t sg) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(seg_empty + sg % C::RING);
+  };
 
   if (warp >= C::MMA_WARP) {
     // ======================= MMA issuer =======================
@@ -266,8 +296,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
       };
       uint32_t k = 0;                                // key tiles used so far
       uint32_t qc = 0, pc = 0;                       // phases of q_full and p_full: bit t
-      while (ok && w.u < w.u_end) {
-        w.next();
+      for (uint32_t sg = 0; (ok = take_segment(sg)); ++sg) {
+        const Kv4Seg& from = segs[sg % C::RING];
+        struct {
+          int kt0, kt1, end[2];
+        } const w{from.kt0, from.kt1, {from.end[0], from.end[1]}};
+        free_segment(sg);
+        if (w.kt0 == w.kt1) break;
         // S of the segment's first tile (issued after the previous segment's last P V on this
         // thread, so it overwrites that P only after it has been read)
 #pragma unroll
@@ -316,49 +351,109 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
           commit(v_empty + (k & 1));
           if (k_ready) commit(k_empty + (k1 & 1));
         }
+        if (!ok) break;
       }
       if (!ok && lane == 0) record_timeout();
       // every MMA this warp issued completes before TMEM can be released
       commit(drain_bar);
       drain_wait(drain_bar, 0, cp.timeout_cycles);
       __syncwarp();
+    } else if (warp == C::WALK_WARP) {
+      // ======================= the walk =======================
+      Kv4ChunkWalk w(p);
+      const Kv4Runs runs(w.total(lane), p.ctas);
+      const bool idle = static_cast<int>(blockIdx.x) >= runs.n;
+      const long long u0 = idle ? 0 : runs.start(blockIdx.x), u1 = idle ? 0 : runs.start(blockIdx.x + 1);
+      if (!idle) w.seek(u0, u1, lane);
+      w.u = u0;
+      w.u_end = u1;
+      if (lane == 0) cp.heads[blockIdx.x].parts = 0;
+      const uint32_t slot_mask = (1u << p.c.page_shift) - 1u;
+      uint32_t k = 0;
+      for (uint32_t sg = 0; ok; ++sg) {
+        const bool over = w.u >= w.u_end, first = w.u == u0;
+        if (!over) w.next();
+        if (sg >= C::RING && !(ok = wait_all(seg_empty + sg % C::RING, (sg / C::RING - 1) & 1u))) break;
+        if (lane == 0) {
+          Kv4Seg x;
+          x.kt0 = over ? 0 : w.kt0, x.kt1 = over ? 0 : w.kt1;
+          x.end[0] = w.end[0], x.end[1] = w.end[1];
+          x.len = w.len, x.n = w.n;
+          x.r0 = w.qp * kChunkRows;
+          x.slot = !over && w.whole() ? -1 : 2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1);
+          x.row = (static_cast<unsigned long long>(w.b) * p.c.H + w.h) * w.R;
+          segs[sg % C::RING] = x;
+          if (!over && w.kt0 == 0 && !w.whole()) {    // the unit's first part: what the join needs
+            Kv4Head hd;
+            hd.parts = runs.cta_of(w.u - w.kt1 + w.nkv - 1) - static_cast<int>(blockIdx.x) + 1;
+            hd.b = w.b, hd.h = w.h, hd.qp = w.qp, hd.slot = x.slot;
+            cp.heads[blockIdx.x] = hd;
+          }
+          mbar_arrive(seg_full + sg % C::RING);
+        }
+        if (over) break;
+        const int* table = p.c.block_table + static_cast<long long>(w.b) * p.c.max_pages;
+        for (int j = w.kt0; j < w.kt1; ++j, ++k) {
+          uint32_t rw[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = j * 128 + 32 * i + lane;
+            rw[i] = key < w.len ? static_cast<uint32_t>(table[key >> p.c.page_shift]) : kNoRow;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = j * 128 + 32 * i + lane;
+            uint32_t row;
+            rw[i] = key < w.len && kv4_row(p.c, static_cast<int>(rw[i]), w.h, key & static_cast<int>(slot_mask), row)
+                        ? row : kNoRow;
+          }
+          const uint32_t at = k % C::RING;
+          if (k >= C::RING && !(ok = wait_all(row_empty + at, (k / C::RING - 1) & 1u))) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) rows[at * 128 + 32 * i + lane] = rw[i];
+          if (lane == 0) edges[at] = w.lim_all - j * 128;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(row_full + at);
+        }
+      }
+      // the conversion warps stop at the tile that says so
+      if (ok) {
+        const uint32_t at = k % C::RING;
+        if (k >= C::RING) ok = wait_all(row_empty + at, (k / C::RING - 1) & 1u);
+        if (lane == 0) {
+          edges[at] = kNoTile;
+          mbar_arrive(row_full + at);
+        }
+      }
+      if (!ok && lane == 0) record_timeout();
+      __syncwarp();
+    } else {
+      kv4_empty_rows<D>(p, threadIdx.x - (C::WALK_WARP + 1) * 32, 64);
     }
   } else if (warp >= C::CONV_WARP) {
     // ======================= codes -> f16 K^ and V^ =======================
     regs_decrease<C::REGS_CONV>();
     const int kr = threadIdx.x - C::CONV_WARP * 32;   // key row of this thread
     constexpr int NW = C::CODE_ROW / 16;              // 16-byte pieces of a row's codes
-    const uint32_t slot_mask = (1u << p.c.page_shift) - 1u;
-    const long long tiles = u1 - u0;
-    // the load position: tile lj of the walk's segment
-    int lj = 0;
-    auto step = [&]() {                               // to the next tile (the first at the first call)
-      if (w.u > u0 && lj + 1 < w.kt1) {
-        ++lj;
-      } else if (w.u < w.u_end) {
-        w.next();
-        lj = w.kt0;
-      }
-    };
-    auto page_of = [&]() {                            // page of this thread's key; what lies behind the end: none
-      const int key = lj * 128 + kr;
-      return key < w.len ? p.c.block_table[static_cast<long long>(w.b) * p.c.max_pages + (key >> p.c.page_shift)] : -1;
-    };
     uint4 kw[NW], vw[NW];
     uint32_t ksf[SfWords<D>::N], vsf_next[SfWords<D>::N], vsf[SfWords<D>::N];
-    uint32_t row = 0;
-    bool valid = false, edge = false;                 // the key exists; some row does not see it
-    // the row of the tile at the load position (its page has been looked up), and K's codes, with the
-    // scales of both
-    auto load_k = [&](int page) {
-      const int key = lj * 128 + kr;
-      valid = key < w.len && kv4_row(p.c, page, w.h, key & static_cast<int>(slot_mask), row);
-      edge = key > w.lim_all;
+    uint32_t row = kNoRow;                            // cache row of this thread's key in the tile loaded last
+    bool edge = false;                                // some row of the unit does not see the key
+    // tile k of the run: its row, K's codes and the scales of both; false: there is none
+    auto load_k = [&](uint32_t k) {
+      const uint32_t at = k % C::RING;
+      if (!(ok = wait_all(row_full + at, (k / C::RING) & 1u))) return false;
+      const int e = edges[at];
+      row = rows[at * 128 + kr];
+      edge = kr > e;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(row_empty + at);
+      if (e == kNoTile) return false;
 #pragma unroll
       for (int i = 0; i < SfWords<D>::N; ++i) ksf[i] = vsf_next[i] = 0u;
 #pragma unroll
       for (int i = 0; i < NW; ++i) kw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (valid) {
+      if (row != kNoRow) {
         const uint4* src = reinterpret_cast<const uint4*>(p.c.codes[0] + static_cast<size_t>(row) * C::CODE_ROW);
 #pragma unroll
         for (int i = 0; i < NW; ++i) kw[i] = __ldg(src + i);
@@ -368,11 +463,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
           vsf_next[i] = __ldg(reinterpret_cast<const uint32_t*>(p.c.sf[1] + static_cast<size_t>(row) * C::SF_ROW) + i);
         }
       }
+      return true;
     };
     auto load_v = [&]() {
 #pragma unroll
       for (int i = 0; i < NW; ++i) vw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (valid) {
+      if (row != kNoRow) {
         const uint4* src = reinterpret_cast<const uint4*>(p.c.codes[1] + static_cast<size_t>(row) * C::CODE_ROW);
 #pragma unroll
         for (int i = 0; i < NW; ++i) vw[i] = __ldg(src + i);
@@ -397,14 +493,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         }
       }
     };
-    int page = -1;
-    if (tiles > 0) {
-      step();
-      load_k(page_of());
-      load_v();
-    }
-    for (long long k = 0; ok && k < tiles; ++k) {
-      const uint32_t buf = static_cast<uint32_t>(k) & 1u, round = static_cast<uint32_t>(k >> 1);
+    bool more = load_k(0);
+    if (more) load_v();
+    for (uint32_t k = 0; more; ++k) {
+      const uint32_t buf = k & 1u, round = k >> 1;
 #pragma unroll
       for (int i = 0; i < SfWords<D>::N; ++i) vsf[i] = vsf_next[i];
       // A NaN value must reach the rows that see it and no other, and P = 0 would not keep it from a
@@ -419,17 +511,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
           for (int i = 0; i < SfWords<D>::N; ++i) ksf[i] = 0x7F7F7F7Fu, vsf[i] = 0u;
         }
       }
-      const bool more = k + 1 < tiles;
-      if (more) {
-        step();
-        page = page_of();
-      }
       if (k >= 2 && !(ok = wait_all(k_empty + buf, (round - 1) & 1))) break;
       convert(kw, ksf, smem + C::SMEM_K + buf * C::TILE_BYTES);
       fence_proxy_async_shared();   // the MMA (async proxy) reads what these threads wrote
       __syncwarp();
       if (lane == 0) mbar_arrive(k_full + buf);
-      if (more) load_k(page);
+      more = load_k(k + 1);
+      if (!ok) break;
       if (k >= 2 && !(ok = wait_all(v_empty + buf, (round - 1) & 1))) break;
       convert(vw, vsf, smem + C::SMEM_V + buf * C::TILE_BYTES);
       fence_proxy_async_shared();
@@ -447,24 +535,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
     const uint32_t s_tm = tmem_base + lane_off + t * 128;
     const uint32_t o_tm = tmem_base + lane_off + C::O_COL0 + t * D;
     uint32_t sc = 0, oc = 0;                          // phases of s_full and o_done
-    while (ok && w.u < w.u_end) {
-      const bool first_segment = w.u == u0;
-      w.next();
-      const bool whole = w.whole();
-      const int rr = w.qp * kChunkRows + t * 128 + r; // row of (b, h)
-      const int slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
+    const int R = p.Hq / p.c.H * p.N;
+    for (uint32_t sg = 0; ok && (ok = take_segment(sg)); ++sg) {
+      const Kv4Seg& w = segs[sg % C::RING];
+      const int kt0 = w.kt0, endt = w.end[t];
+      if (kt0 == w.kt1) break;
+      const bool whole = w.slot < 0;
+      const int rr = w.r0 + t * 128 + r;              // row of (b, h)
       const int i_tok = rr % p.N;
-      const size_t row = (static_cast<size_t>(w.b) * p.c.H + w.h) * w.R + rr;
-      const size_t prow = static_cast<size_t>(slot) * kChunkRows + t * 128 + r;
-      if (w.kt0 == 0 && !whole && threadIdx.x == 0) { // the unit's first part: what the join needs
-        const long long unit0 = w.u - w.kt1;
-        Kv4Head hd;
-        hd.parts = runs.cta_of(unit0 + w.nkv - 1) - static_cast<int>(blockIdx.x) + 1;
-        hd.b = w.b, hd.h = w.h, hd.qp = w.qp, hd.slot = slot;
-        cp.heads[blockIdx.x] = hd;
-      }
-      const int endt = t == 0 ? w.end[0] : w.end[1];
-      if (endt <= w.kt0) {
+      const bool have = rr < R, write = have && i_tok < w.n;
+      const size_t row = w.row + rr;
+      const size_t prow = static_cast<size_t>(whole ? 0 : w.slot) * kChunkRows + t * 128 + r;
+      // last key this row sees (rows that hold no query see everything: they are not written)
+      const int lim = p.causal && i_tok < w.n ? w.len - w.n + i_tok : w.len - 1;
+      free_segment(sg);
+      if (endt <= kt0) {
         if (!whole) p.part_ml[prow] = make_float2(-INFINITY, 0.f);
         continue;
       }
@@ -474,7 +559,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
       {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D * 2);
         float amax = 0.f;
-        const bool have = rr < w.R;
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
           const uint4 x = have ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
@@ -505,10 +589,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         fence_proxy_async_shared();
         mbar_arrive(q_full + t);
       }
-      // last key this row sees (rows that hold no query see everything: they are not written)
-      const int lim = p.causal && i_tok < w.n ? w.len - w.n + i_tok : w.len - 1;
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = w.kt0; j < endt; ++j) {
+      for (int j = kt0; j < endt; ++j) {
         if (!(ok = wait_all(s_full + t, sc & 1))) break;
         ++sc;
         tc_fence_after();
@@ -529,7 +611,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         if (m_blk - m_run > C::RESCALE_THRESHOLD) m_use = m_blk;
         const bool moved = m_use != m_run;
         const float alpha = moved ? ex2_approx(m_run - m_use) : 1.f;
-        if (j > w.kt0 && __any_sync(0xffffffffu, moved)) {
+        if (j > kt0 && __any_sync(0xffffffffu, moved)) {
 #pragma unroll
           for (int cb = 0; cb < D; cb += 32) {
             uint32_t ov[32];
@@ -550,7 +632,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
       ++oc;
       tc_fence_after();
       const float f = whole ? (l_run == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / l_run) : 1.f;
-      const bool write = whole ? rr < w.R && i_tok < w.n : true;
 #pragma unroll
       for (int cb = 0; cb < D; cb += 32) {
         uint32_t ov[32];
