@@ -114,9 +114,9 @@ attn_status launch_kv4_dec(const attn::Kv4AttnParams& p, int tag, cudaStream_t s
   return ATTN_OK;
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool PAIR>
 attn_status launch_kv4_chunk(const attn::Kv4AttnParams& p, const Kv4Plan& plan, int tag, cudaStream_t stream) {
-  using C = attn::Kv4ChunkCfg<D>;
+  using C = attn::Kv4ChunkCfg<D, PAIR>;
   auto kern = attn::kv4_chunk_sm100<C, F16>;
   if (!set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, tag)) return ATTN_ERR_CUDA;
   attn::Kv4ChunkParams cp;
@@ -124,7 +124,7 @@ attn_status launch_kv4_chunk(const attn::Kv4AttnParams& p, const Kv4Plan& plan, 
   cp.heads = reinterpret_cast<attn::Kv4Head*>(reinterpret_cast<uint8_t*>(p.part_o) + plan.o_bytes);
   cp.timeout_cycles = kWaitLimitCycles;
   kern<<<p.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(cp);
-  const cudaError_t e = launch_after(attn::kv4_chunk_join_sm100<C, F16>, dim3(p.ctas, attn::kChunkRows / 32), 256, stream, cp);
+  const cudaError_t e = launch_after(attn::kv4_chunk_join_sm100<C, F16>, dim3(p.ctas, (PAIR ? 128 : attn::kChunkRows) / 8), 256, stream, cp);
   if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) {
     forget_smem(tag);
     return ATTN_ERR_CUDA;
@@ -134,8 +134,10 @@ attn_status launch_kv4_chunk(const attn::Kv4AttnParams& p, const Kv4Plan& plan, 
 
 template <int D, bool F16>
 attn_status launch_kv4_rows(const attn::Kv4AttnParams& p, const Kv4Plan& plan, cudaStream_t stream) {
-  const int tag = 16 + (D == 128 ? 0 : 8) + (F16 ? 4 : 0);
-  if (plan.nt == 0) return launch_kv4_chunk<D, F16>(p, plan, tag + 3, stream);
+  const int tag = 16 + (D == 128 ? 0 : 10) + (F16 ? 5 : 0);
+  if (plan.nt == 0)
+    return p.Hq / p.c.H * p.N <= 128 ? launch_kv4_chunk<D, F16, true>(p, plan, tag + 3, stream)
+                                     : launch_kv4_chunk<D, F16, false>(p, plan, tag + 4, stream);
   if (plan.nt == 1) return launch_kv4_dec<attn::Kv4DecCfg<D, 1>, F16>(p, tag, stream);
   if (plan.nt == 2) return launch_kv4_dec<attn::Kv4DecCfg<D, 2>, F16>(p, tag + 1, stream);
   return launch_kv4_dec<attn::Kv4DecCfg<D, 4>, F16>(p, tag + 2, stream);

@@ -17,6 +17,10 @@
 //    equal work whatever the lengths. A unit that several runs share is joined by
 //    kv4_chunk_join_sm100 from fp32 parts in the workspace, in the order of the runs.
 //
+//  * With at most 128 rows (PAIR) a unit has one row tile, which would leave one softmax group idle and
+//    make every step a chain; there both groups work on the same rows, group t on every second key
+//    tile, and group 0 joins the two results from tensor memory at the segment's end.
+//
 // CTA: 16 warps. 0-3 softmax of tile 0, 4-7 of tile 1, 8-11 conversion, 12 MMA issuer (owns
 // TMEM), 13 walks the run: it hands out the segments (a unit's tiles [kt0, kt1)) and, tile by
 // tile, the cache row of every key through small rings in shared memory, so that neither the page
@@ -32,9 +36,10 @@
 
 namespace attn {
 
-template <int D_>
+template <int D_, bool PAIR_>
 struct Kv4ChunkCfg {
   static constexpr int D = D_;
+  static constexpr bool PAIR = PAIR_;                           // at most 128 rows of a cached head
   static constexpr int CHUNKS = D / 64;                         // 128-byte column chunks of a row of f16
   static constexpr int CHUNK_BYTES = 128 * 128;
   static constexpr int TILE_BYTES = CHUNKS * CHUNK_BYTES;       // 128 rows of f16
@@ -44,8 +49,8 @@ struct Kv4ChunkCfg {
   static constexpr bool PV_F16 = true;
   static constexpr int THREADS = 512;
   static constexpr int CONV_WARP = 8, MMA_WARP = 12, WALK_WARP = 13;
-  // launch: 65536 / 512 = 128 registers a thread; 2 * 128 * 184 + 128 * 88 + 128 * 56 = 65536
-  static constexpr uint32_t REGS_SOFTMAX = 184, REGS_CONV = 88, REGS_MMA = 56;
+  // launch: 65536 / 512 = 128 registers a thread; 2 * 128 * 184 + 128 * 96 + 128 * 48 = 65536
+  static constexpr uint32_t REGS_SOFTMAX = 184, REGS_CONV = 96, REGS_MMA = 48;
   static_assert(2 * REGS_SOFTMAX + REGS_CONV + REGS_MMA <= 512, "register split");
   static constexpr uint32_t TMEM_COLS = 512, O_COL0 = 256;
   static constexpr float RESCALE_THRESHOLD = 8.0f;
@@ -55,12 +60,14 @@ struct Kv4ChunkCfg {
   static constexpr int SMEM_BAR = 6 * TILE_BYTES;
   static constexpr int RING = 4;                                // segments, and tiles, handed out ahead
   // q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_done[2], drain,
-  // seg_full[RING], seg_empty[RING], row_full[RING], row_empty[RING]
-  static constexpr int NUM_BARS = 2 * 7 + 4 + 1 + 4 * RING;
+  // seg_full[RING], seg_empty[RING], row_full[RING], row_empty[RING], xch_full, xch_empty
+  static constexpr int NUM_BARS = 2 * 7 + 4 + 1 + 4 * RING + 2;
   static constexpr int SMEM_MISC = SMEM_BAR + (NUM_BARS + 1) / 2 * 16;
   static constexpr int SMEM_SEG = SMEM_MISC + 16;               // Kv4Seg[RING]
   static constexpr int SMEM_ROWS = SMEM_SEG + RING * 64;        // [RING][128] cache rows, [RING] first edge key
-  static constexpr int SMEM_BYTES = SMEM_ROWS + RING * (128 + 4) * 4 + 1024;
+  static constexpr int SMEM_XCH = SMEM_ROWS + RING * (128 + 4) * 4;       // PAIR: [128] (max, sum) of group 1
+  static constexpr int SMEM_BYTES = SMEM_XCH + 128 * 8 + 1024;
+  static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 };
 constexpr int kChunkRows = 256;
 
@@ -215,6 +222,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
   uint64_t* seg_empty = seg_full + C::RING;
   uint64_t* row_full = seg_empty + C::RING;
   uint64_t* row_empty = row_full + C::RING;
+  uint64_t* xch_full = row_empty + C::RING;          // PAIR: group 1's result is complete
+  uint64_t* xch_empty = xch_full + 1;                // and has been read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC);
   uint32_t* abort_word = tmem_slot + 1;
   Kv4Seg* segs = reinterpret_cast<Kv4Seg*>(smem + C::SMEM_SEG);
@@ -243,6 +252,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
       mbar_init(row_full + i, 1);
       mbar_init(row_empty + i, 4);                   // conversion warps
     }
+    mbar_init(xch_full, 128);
+    mbar_init(xch_empty, 128);
     *abort_word = 0u;
     fence_barrier_init();
     fence_proxy_async_shared();
@@ -277,8 +288,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
       const uint32_t q_lo = smem_desc_lo(smem_addr(smem + C::SMEM_Q), 16);
       const uint32_t k_lo = smem_desc_lo(smem_addr(smem + C::SMEM_K), 16);
       const uint32_t v_lo = smem_desc_lo(smem_addr(smem + C::SMEM_V), C::CHUNK_BYTES);
-      auto issue_s = [&](int t, uint32_t buf) {
-        const uint32_t qa = q_lo + ((t * C::TILE_BYTES) >> 4), ka = k_lo + ((buf * C::TILE_BYTES) >> 4);
+      auto issue_s = [&](int t, uint32_t buf) {      // S_t; PAIR: of the one q tile
+        const uint32_t qa = q_lo + (((C::PAIR ? 0 : t) * C::TILE_BYTES) >> 4), ka = k_lo + ((buf * C::TILE_BYTES) >> 4);
 #pragma unroll
         for (int kk = 0; kk < C::S_KSTEPS; ++kk) {
           const uint32_t off = ((kk / 4) * C::CHUNK_BYTES + (kk % 4) * 32) >> 4;
@@ -303,6 +314,39 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         } const w{from.kt0, from.kt1, {from.end[0], from.end[1]}};
         free_segment(sg);
         if (w.kt0 == w.kt1) break;
+        if constexpr (C::PAIR) {
+          // group t takes the segment's key tiles t, t + 2, ...: S of the first two, then for each tile
+          // its P V and the S of the next but one
+          auto s_of = [&](int t, uint32_t x) -> bool {     // S_t of the run's key tile x
+            if (!wait_all(k_full + (x & 1), (x >> 1) & 1)) return false;
+            tc_fence_after();
+            issue_s(t, x & 1);
+            commit(s_full + t);
+            commit(k_empty + (x & 1));
+            return true;
+          };
+          const int nt = w.kt1 - w.kt0;
+          if (!(ok = wait_all(q_full, qc & 1u))) break;
+          qc ^= 1u;
+          if (!(ok = s_of(0, k)) || (nt > 1 && !(ok = s_of(1, k + 1)))) break;
+          for (int j = 0; j < nt; ++j, ++k) {
+            const int t = j & 1;
+            if (!(ok = wait_all(v_full + (k & 1), (k >> 1) & 1))) break;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (!(ok = wait_all(p_full + 2 * t + c, (pc >> t) & 1u))) break;
+              tc_fence_after();
+              issue_pv(t, k & 1, c, j > 1 || c > 0);
+            }
+            if (!ok) break;
+            pc ^= 1u << t;
+            if (j + 2 >= nt) commit(o_done + t);
+            commit(v_empty + (k & 1));
+            if (j + 2 < nt && !(ok = s_of(t, k + 2))) break;
+          }
+          if (!ok) break;
+          continue;
+        }
         // S of the segment's first tile (issued after the previous segment's last P V on this
         // thread, so it overwrites that P only after it has been read)
 #pragma unroll
@@ -536,28 +580,40 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
     const uint32_t o_tm = tmem_base + lane_off + C::O_COL0 + t * D;
     uint32_t sc = 0, oc = 0;                          // phases of s_full and o_done
     const int R = p.Hq / p.c.H * p.N;
+    uint32_t xc = 0;                                  // PAIR: segments so far (phases of xch_full, xch_empty)
+    float2* xch = reinterpret_cast<float2*>(smem + C::SMEM_XCH);
     for (uint32_t sg = 0; ok && (ok = take_segment(sg)); ++sg) {
       const Kv4Seg& w = segs[sg % C::RING];
-      const int kt0 = w.kt0, endt = w.end[t];
-      if (kt0 == w.kt1) break;
+      const int kt0 = w.kt0, kt1 = w.kt1;
+      if (kt0 == kt1) break;
       const bool whole = w.slot < 0;
-      const int rr = w.r0 + t * 128 + r;              // row of (b, h)
+      // this group's row tile and key tiles
+      const int ta = C::PAIR ? 0 : t, j0 = kt0 + (C::PAIR ? t : 0), endt = C::PAIR ? kt1 : w.end[t];
+      constexpr int STEP = C::PAIR ? 2 : 1;
+      const int rr = w.r0 + ta * 128 + r;             // row of (b, h)
       const int i_tok = rr % p.N;
       const bool have = rr < R, write = have && i_tok < w.n;
       const size_t row = w.row + rr;
-      const size_t prow = static_cast<size_t>(whole ? 0 : w.slot) * kChunkRows + t * 128 + r;
+      const size_t prow = static_cast<size_t>(whole ? 0 : w.slot) * kChunkRows + ta * 128 + r;
       // last key this row sees (rows that hold no query see everything: they are not written)
       const int lim = p.causal && i_tok < w.n ? w.len - w.n + i_tok : w.len - 1;
       free_segment(sg);
-      if (endt <= kt0) {
+      if (!C::PAIR && endt <= j0) {
         if (!whole) p.part_ml[prow] = make_float2(-INFINITY, 0.f);
         continue;
       }
       // ---- the row's q: scaled by a power of two, f16, into the tile's swizzled rows. Every S
-      // MMA that read the previous q has completed: this thread saw the last one's barrier.
-      float c;
-      {
+      // MMA that read the previous q has completed: this thread saw the last one's barrier (or, for group
+      // 1's of a PAIR segment, group 1's result). PAIR: group 0 writes it for both. Two passes over the
+      // row, which the prefetch brings into L1 at the cost of one memory latency and no registers.
+      float c = 1.f;
+      if (j0 < endt) {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D * 2);
+        if (have) {
+#pragma unroll
+          for (int i = 0; i < D * 2; i += 128)
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(src) + i));
+        }
         float amax = 0.f;
 #pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
@@ -572,25 +628,27 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         const int e2 = kv4_row_exp(amax);
         const float down = __int_as_float((254 - e2) << 23);
         c = fmaxf(__int_as_float(e2 << 23) * p.scale_log2, 1e-37f);
-        uint8_t* qrow = smem + C::SMEM_Q + t * C::TILE_BYTES + r * 128;
+        if (!C::PAIR || t == 0) {
+          uint8_t* qrow = smem + C::SMEM_Q + ta * C::TILE_BYTES + r * 128;
 #pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = have ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-          uint32_t y[4];
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 x = have ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = f32x2_from_16<F16>(xs[e]);
-            y[e] = pack_f16x2(f.x * down, f.y * down);
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = f32x2_from_16<F16>(xs[e]);
+              y[e] = pack_f16x2(f.x * down, f.y * down);
+            }
+            *reinterpret_cast<uint4*>(qrow + (i >> 3) * C::CHUNK_BYTES + (((i & 7) ^ (r & 7)) << 4)) =
+                make_uint4(y[0], y[1], y[2], y[3]);
           }
-          *reinterpret_cast<uint4*>(qrow + (i >> 3) * C::CHUNK_BYTES + (((i & 7) ^ (r & 7)) << 4)) =
-              make_uint4(y[0], y[1], y[2], y[3]);
+          fence_proxy_async_shared();
+          mbar_arrive(q_full + ta);
         }
-        fence_proxy_async_shared();
-        mbar_arrive(q_full + t);
       }
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = kt0; j < endt; ++j) {
+      for (int j = j0; j < endt; j += STEP) {
         if (!(ok = wait_all(s_full + t, sc & 1))) break;
         ++sc;
         tc_fence_after();
@@ -611,7 +669,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         if (m_blk - m_run > C::RESCALE_THRESHOLD) m_use = m_blk;
         const bool moved = m_use != m_run;
         const float alpha = moved ? ex2_approx(m_run - m_use) : 1.f;
-        if (j > kt0 && __any_sync(0xffffffffu, moved)) {
+        if (j > j0 && __any_sync(0xffffffffu, moved)) {
 #pragma unroll
           for (int cb = 0; cb < D; cb += 32) {
             uint32_t ov[32];
@@ -628,20 +686,59 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         m_run = m_use;
       }
       if (!ok) break;
-      if (!(ok = wait_all(o_done + t, oc & 1))) break;
-      ++oc;
-      tc_fence_after();
-      const float f = whole ? (l_run == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / l_run) : 1.f;
+      if (!C::PAIR || j0 < endt) {
+        if (!(ok = wait_all(o_done + t, oc & 1))) break;
+        ++oc;
+        tc_fence_after();
+      }
+      float f0 = 1.f, f1 = 0.f;                       // factors of this group's O and of group 1's
+      if constexpr (C::PAIR) {
+        const uint32_t ph = xc & 1u;
+        ++xc;
+        if (t == 1) {                                 // hands its result over, and waits until it has been read
+          xch[r] = make_float2(m_run, l_run);
+          tc_fence_before();
+          mbar_arrive(xch_full);
+          if (!(ok = wait_all(xch_empty, ph))) break;
+          tc_fence_after();
+          continue;
+        }
+        if (!(ok = wait_all(xch_full, ph))) break;
+        tc_fence_after();
+        const float2 x = xch[r];
+        const float M = fmaxf(m_run, x.x), Mu = M == -INFINITY ? 0.f : M;
+        f0 = ex2_approx(m_run - Mu);
+        f1 = ex2_approx(x.x - Mu);
+        l_run = l_run * f0 + x.y * f1;
+        m_run = M;
+      }
+      if (whole) {
+        const float inv = l_run == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / l_run;
+        f0 *= inv;
+        f1 *= inv;
+      }
+      const bool join = C::PAIR && kt1 - kt0 > 1;     // group 1 had a tile
 #pragma unroll
       for (int cb = 0; cb < D; cb += 32) {
         uint32_t ov[32];
         tmem_ld32(o_tm + cb, ov);
         tmem_ld_wait<32>(ov);
+        if (C::PAIR || whole) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f0);
+        }
+        if (join) {
+          uint32_t o1[32];
+          tmem_ld32(o_tm + D + cb, o1);
+          tmem_ld_wait<32>(o1);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            ov[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(ov[i])));
+        }
         if (whole) {
           uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            pk[i] = pack_16<F16>(__uint_as_float(ov[2 * i]) * f, __uint_as_float(ov[2 * i + 1]) * f);
+          for (int i = 0; i < 16; ++i) pk[i] = pack_16<F16>(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1]));
           if (write) {
             uint4* dst = reinterpret_cast<uint4*>(p.o + (row * D + cb) * 2);
 #pragma unroll
@@ -652,6 +749,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
 #pragma unroll
           for (int i = 0; i < 8; ++i) dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
         }
+      }
+      if constexpr (C::PAIR) {
+        tc_fence_before();
+        mbar_arrive(xch_empty);
       }
       if (!whole) p.part_ml[prow] = make_float2(m_run, l_run);
       else if (p.lse != nullptr && write)
@@ -667,8 +768,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
   if (warp == C::MMA_WARP) tmem_dealloc(tmem_base, C::TMEM_COLS);
 }
 
-// Joins the parts of the unit whose first part CTA blockIdx.x wrote: 32 rows per block of 256
-// threads, a warp per row at a time, D / 32 channels a lane.
+// Joins the parts of the unit whose first part CTA blockIdx.x wrote: a warp per row. A lane holds the
+// (maximum, sum) of one part, so that the parts' O, D / 32 channels a lane, load without waiting for
+// one another.
 template <class C, bool F16>
 __global__ void __launch_bounds__(256) kv4_chunk_join_sm100(const Kv4ChunkParams cp) {
   constexpr int D = C::D, E = D / 32;
@@ -678,32 +780,45 @@ __global__ void __launch_bounds__(256) kv4_chunk_join_sm100(const Kv4ChunkParams
   if (hd.parts == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int R = p.Hq / p.c.H * p.N, n = kv4_qlen(p, hd.b);
-  for (int k = warp; k < 32; k += 8) {
-    const int r = blockIdx.y * 32 + k, rr = hd.qp * kChunkRows + r;
-    if (rr >= R || rr % p.N >= n) continue;
-    float M = -INFINITY, L = 0.f, a[E] = {};
-#pragma unroll 4
-    for (int i = 0; i < hd.parts; ++i) {
-      const size_t at = static_cast<size_t>(i == 0 ? hd.slot : 2 * (static_cast<int>(blockIdx.x) + i)) * kChunkRows + r;
-      const float2 x = __ldcg(p.part_ml + at);
-      if (x.x == -INFINITY && x.y == 0.f) continue;   // the part's keys lie behind this row's (nothing written)
-      float v[E];
+  const int r = blockIdx.y * 8 + warp, rr = hd.qp * kChunkRows + r;
+  if (rr >= R || rr % p.N >= n) return;
+  float M = -INFINITY, L = 0.f, a[E] = {};
+  for (int i0 = 0; i0 < hd.parts; i0 += 32) {
+    auto at = [&](int i) {
+      return static_cast<size_t>(i == 0 ? hd.slot : 2 * (static_cast<int>(blockIdx.x) + i)) * kChunkRows + r;
+    };
+    const int i = i0 + lane;
+    const float2 x = i < hd.parts ? __ldcg(p.part_ml + at(i)) : make_float2(-INFINITY, 0.f);
+    float mx = x.x;
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = __ldcg(p.part_o + at * D + lane + 32 * e);
-      const float Mn = fmaxf(M, x.x), Mu = Mn == -INFINITY ? 0.f : Mn;
-      const float fo = b200::ex2_approx(M - Mu), fn = b200::ex2_approx(x.x - Mu);
-      L = L * fo + x.y * fn;
+    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    const float Mn = fmaxf(M, mx), Mu = Mn == -INFINITY ? 0.f : Mn;
+    const float fo = b200::ex2_approx(M - Mu), mine = b200::ex2_approx(x.x - Mu);
+    // (a part whose keys lie behind this row's has no O: nothing was written)
+    const uint32_t full = __ballot_sync(0xffffffffu, !(x.x == -INFINITY && x.y == 0.f));
+    float sum = x.y * mine;
 #pragma unroll
-      for (int e = 0; e < E; ++e) a[e] = a[e] * fo + v[e] * fn;
-      M = Mn;
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    L = L * fo + sum;
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] *= fo;
+    const int m = min(32, hd.parts - i0);
+#pragma unroll 8
+    for (int k = 0; k < m; ++k) {
+      const float f = __shfl_sync(0xffffffffu, mine, k);
+      const bool have = (full >> k) & 1u;
+      const float* src = p.part_o + at(i0 + k) * D + lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] += f * (have ? __ldcg(src + 32 * e) : 0.f);
     }
-    const float inv = L == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / L;
-    const size_t row = (static_cast<size_t>(hd.b) * p.c.H + hd.h) * R + rr;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      reinterpret_cast<uint16_t*>(p.o)[row * D + lane + 32 * e] = static_cast<uint16_t>(pack_16<F16>(a[e] * inv, 0.f));
-    if (p.lse != nullptr && lane == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+    M = Mn;
   }
+  const float inv = L == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / L;
+  const size_t row = (static_cast<size_t>(hd.b) * p.c.H + hd.h) * R + rr;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    reinterpret_cast<uint16_t*>(p.o)[row * D + lane + 32 * e] = static_cast<uint16_t>(pack_16<F16>(a[e] * inv, 0.f));
+  if (p.lse != nullptr && lane == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
 }
 
 }  // namespace attn
