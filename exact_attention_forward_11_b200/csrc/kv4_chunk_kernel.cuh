@@ -580,69 +580,88 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
     const uint32_t o_tm = tmem_base + lane_off + C::O_COL0 + t * D;
     uint32_t sc = 0, oc = 0;                          // phases of s_full and o_done
     const int R = p.Hq / p.c.H * p.N;
+    // The warp's 32 rows of its tile's q also stage its output: row i holds UPR 16-byte units, RPI rows
+    // make 32 of them.
+    constexpr int UPR = D / 8, RPI = 32 / UPR;
+    // (the thread's place is read anew, opaquely, where a segment begins and ends: what is derived from it
+    // would otherwise be kept in registers through the tile loop, which spills for it)
+    auto thread_here = [] {
+      uint32_t x;
+      asm volatile("mov.u32 %0, %%tid.x;" : "=r"(x));
+      return static_cast<int>(x);
+    };
     uint32_t xc = 0;                                  // PAIR: segments so far (phases of xch_full, xch_empty)
     float2* xch = reinterpret_cast<float2*>(smem + C::SMEM_XCH);
     for (uint32_t sg = 0; ok && (ok = take_segment(sg)); ++sg) {
-      const Kv4Seg& w = segs[sg % C::RING];
-      const int kt0 = w.kt0, kt1 = w.kt1;
-      if (kt0 == kt1) break;
-      const bool whole = w.slot < 0;
-      // this group's row tile and key tiles
-      const int ta = C::PAIR ? 0 : t, j0 = kt0 + (C::PAIR ? t : 0), endt = C::PAIR ? kt1 : w.end[t];
-      constexpr int STEP = C::PAIR ? 2 : 1;
-      const int rr = w.r0 + ta * 128 + r;             // row of (b, h)
-      const int i_tok = rr % p.N;
-      const bool have = rr < R, write = have && i_tok < w.n;
-      const size_t row = w.row + rr;
-      const size_t prow = static_cast<size_t>(whole ? 0 : w.slot) * kChunkRows + ta * 128 + r;
-      // last key this row sees (rows that hold no query see everything: they are not written)
-      const int lim = p.causal && i_tok < w.n ? w.len - w.n + i_tok : w.len - 1;
-      free_segment(sg);
-      if (!C::PAIR && endt <= j0) {
-        if (!whole) p.part_ml[prow] = make_float2(-INFINITY, 0.f);
-        continue;
+      // (read again after the tile loop, which has no registers to spare for the segment's fields)
+      volatile const Kv4Seg& w = segs[sg % C::RING];
+      const int j0 = w.kt0 + (C::PAIR ? t : 0), endt = C::PAIR ? w.kt1 : w.end[t];   // this group's key tiles:
+      constexpr int STEP = C::PAIR ? 2 : 1;                                            // j0, j0 + STEP, ... < endt
+      if (w.kt0 == w.kt1) break;
+      int lim;                                        // last key this row sees
+      {
+        const int here = thread_here(), tile_row = C::PAIR ? here & 127 : here & 255;
+        const int i_tok = (w.r0 + tile_row) % p.N;    // (rows that hold no query see everything: they are not written)
+        lim = p.causal && i_tok < w.n ? w.len - w.n + i_tok : w.len - 1;
+        if (!C::PAIR && endt <= j0) {
+          if (w.slot >= 0) p.part_ml[static_cast<size_t>(w.slot) * kChunkRows + tile_row] = make_float2(-INFINITY, 0.f);
+          free_segment(sg);
+          continue;
+        }
       }
-      // ---- the row's q: scaled by a power of two, f16, into the tile's swizzled rows. Every S
-      // MMA that read the previous q has completed: this thread saw the last one's barrier (or, for group
-      // 1's of a PAIR segment, group 1's result). PAIR: group 0 writes it for both. Two passes over the
-      // row, which the prefetch brings into L1 at the cost of one memory latency and no registers.
+      // ---- q: every row scaled by a power of two, f16, into the tile's swizzled rows. The warp loads its
+      // 32 rows together (whole rows to consecutive lanes: a thread reading its own row would touch 32
+      // lines per load). Every S MMA that read the previous q has completed: this warp saw the last one's
+      // barrier (or, for group 1's, group 1's result). PAIR: group 0 writes it for both.
       float c = 1.f;
       if (j0 < endt) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D * 2);
-        if (have) {
-#pragma unroll
-          for (int i = 0; i < D * 2; i += 128)
-            asm volatile("prefetch.global.L1 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(src) + i));
-        }
-        float amax = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = have ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = f32x2_from_16<F16>(xs[e]);
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        const int here = thread_here(), lane = here & 31, wq = (here >> 5) & 3, ta = C::PAIR ? 0 : here >> 7;
+        uint8_t* const tile_rows = smem + C::SMEM_Q + ta * C::TILE_BYTES + wq * 32 * 128;
+        auto unit_at = [&](int i, int u) {
+          return tile_rows + (u >> 3) * C::CHUNK_BYTES + i * 128 + (((u & 7) ^ (i & 7)) << 4);
+        };
+        const int row0 = w.r0 + ta * 128 + wq * 32;   // the warp's first row in (b, h), and in q
+        const unsigned long long qrow0 = w.row + row0;
+        int e_mine = 127;
+#pragma unroll 1
+        for (int it0 = 0; it0 < UPR; it0 += 8) {
+          uint4 x[8];                                 // (in flight together; the loop over them is not unrolled,
+#pragma unroll                                        // which cost the tile loop registers: 1.13 against 1.05 ms)
+          for (int k = 0; k < 8; ++k) {
+            const int i = (it0 + k) * RPI + lane / UPR;                  // row of the warp
+            x[k] = row0 + i < R ? __ldg(reinterpret_cast<const uint4*>(p.q) + (qrow0 + i) * UPR + lane % UPR)
+                                : make_uint4(0u, 0u, 0u, 0u);
           }
-        }
-        const int e2 = kv4_row_exp(amax);
-        const float down = __int_as_float((254 - e2) << 23);
-        c = fmaxf(__int_as_float(e2 << 23) * p.scale_log2, 1e-37f);
-        if (!C::PAIR || t == 0) {
-          uint8_t* qrow = smem + C::SMEM_Q + ta * C::TILE_BYTES + r * 128;
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 x = have ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-            uint32_t y[4];
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {
+            const int it = it0 + k;
+            uint32_t xs[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+#pragma unroll
+            for (int s = 1; s < 8; ++s) x[s - 1] = x[s];
+            float amax = 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 f = f32x2_from_16<F16>(xs[e]);
-              y[e] = pack_f16x2(f.x * down, f.y * down);
+              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
-            *reinterpret_cast<uint4*>(qrow + (i >> 3) * C::CHUNK_BYTES + (((i & 7) ^ (r & 7)) << 4)) =
-                make_uint4(y[0], y[1], y[2], y[3]);
+#pragma unroll
+            for (int sft = 1; sft < UPR; sft <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, sft));
+            const int e2 = kv4_row_exp(amax);
+            const int got = __shfl_sync(0xffffffffu, e2, (lane % RPI) * UPR);
+            if (lane / RPI == it) e_mine = got;
+            if (!C::PAIR || t == 0) {
+              const float down = __int_as_float((254 - e2) << 23);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = f32x2_from_16<F16>(xs[e]);
+                xs[e] = pack_f16x2(f.x * down, f.y * down);
+              }
+              *reinterpret_cast<uint4*>(unit_at(it * RPI + lane / UPR, lane % UPR)) = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+            }
           }
+        }
+        c = fmaxf(__int_as_float(e_mine << 23) * p.scale_log2, 1e-37f);
+        if (!C::PAIR || t == 0) {
           fence_proxy_async_shared();
           mbar_arrive(q_full + ta);
         }
@@ -691,6 +710,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         ++oc;
         tc_fence_after();
       }
+      const int here = thread_here(), lane = here & 31, wq = (here >> 5) & 3, ta = C::PAIR ? 0 : here >> 7;
+      const int r = wq * 32 + lane;
+      uint8_t* const tile_rows = smem + C::SMEM_Q + ta * C::TILE_BYTES + wq * 32 * 128;
+      auto unit_at = [&](int i, int u) {
+        return tile_rows + (u >> 3) * C::CHUNK_BYTES + i * 128 + (((u & 7) ^ (i & 7)) << 4);
+      };
+      const bool whole = w.slot < 0;
+      const int row0 = w.r0 + ta * 128 + wq * 32;
+      const unsigned long long qrow0 = w.row + row0;
+      const bool write = row0 + lane < R && (row0 + lane) % p.N < w.n;
+      const size_t prow = static_cast<size_t>(whole ? 0 : w.slot) * kChunkRows + ta * 128 + r;
       float f0 = 1.f, f1 = 0.f;                       // factors of this group's O and of group 1's
       if constexpr (C::PAIR) {
         const uint32_t ph = xc & 1u;
@@ -701,6 +731,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
           mbar_arrive(xch_full);
           if (!(ok = wait_all(xch_empty, ph))) break;
           tc_fence_after();
+          free_segment(sg);
           continue;
         }
         if (!(ok = wait_all(xch_full, ph))) break;
@@ -717,7 +748,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         f0 *= inv;
         f1 *= inv;
       }
-      const bool join = C::PAIR && kt1 - kt0 > 1;     // group 1 had a tile
+      const bool join = C::PAIR && w.kt1 - w.kt0 > 1; // group 1 had a tile
+      // O leaves through the warp's rows of the q tile (its S MMAs are complete), so that whole rows go to
+      // consecutive lanes: 16 bits in one turn, fp32 parts half a row at a time
+      const uint32_t wmask = __ballot_sync(0xffffffffu, write);
+      uint8_t* const gout = whole ? p.o + qrow0 * D * 2
+                                  : reinterpret_cast<uint8_t*>(p.part_o + (prow - lane) * static_cast<size_t>(D));
 #pragma unroll
       for (int cb = 0; cb < D; cb += 32) {
         uint32_t ov[32];
@@ -736,18 +772,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
             ov[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(ov[i])));
         }
         if (whole) {
-          uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = pack_16<F16>(__uint_as_float(ov[2 * i]), __uint_as_float(ov[2 * i + 1]));
-          if (write) {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + (row * D + cb) * 2);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t pk[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+            for (int e = 0; e < 4; ++e)
+              pk[e] = pack_16<F16>(__uint_as_float(ov[8 * i + 2 * e]), __uint_as_float(ov[8 * i + 2 * e + 1]));
+            *reinterpret_cast<uint4*>(unit_at(lane, cb / 8 + i)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * D + cb);
+          const int cu = (cb % (D / 2)) / 4;          // first unit of these columns in their half
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(unit_at(lane, cu + i)) =
+                make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+        }
+        if (whole ? cb + 32 == D : (cb + 32) % (D / 2) == 0) {
+          __syncwarp();
+          const int bytes = whole ? D * 2 : D * 4, first = whole ? 0 : (cb / (D / 2)) * D * 2;
+#pragma unroll 4
+          for (int it = 0; it < UPR; ++it) {
+            const int i = it * RPI + lane / UPR;
+            const uint4 x = *reinterpret_cast<const uint4*>(unit_at(i, lane % UPR));
+            if (!whole || ((wmask >> i) & 1u))
+              *reinterpret_cast<uint4*>(gout + static_cast<size_t>(i) * bytes + first + (lane % UPR) * 16) = x;
+          }
+          __syncwarp();
         }
       }
       if constexpr (C::PAIR) {
@@ -756,7 +806,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
       }
       if (!whole) p.part_ml[prow] = make_float2(m_run, l_run);
       else if (p.lse != nullptr && write)
-        p.lse[row] = l_run == 0.f ? -INFINITY : (m_run + __log2f(l_run)) * 0.69314718055994531f;
+        p.lse[qrow0 + lane] = l_run == 0.f ? -INFINITY : (m_run + __log2f(l_run)) * 0.69314718055994531f;
+      free_segment(sg);
     }
     if (!ok) record_timeout();
   }
