@@ -66,7 +66,8 @@ struct Kv4ChunkCfg {
   static constexpr int SMEM_SEG = SMEM_MISC + 16;               // Kv4Seg[RING]
   static constexpr int SMEM_ROWS = SMEM_SEG + RING * 64;        // [RING][128] cache rows, [RING] first edge key
   static constexpr int SMEM_XCH = SMEM_ROWS + RING * (128 + 4) * 4;       // PAIR: [128] (max, sum) of group 1
-  static constexpr int SMEM_BYTES = SMEM_XCH + 128 * 8 + 1024;
+  static constexpr int SMEM_STAGE = SMEM_XCH + 128 * 8;         // output rows: 2 KB per softmax warp
+  static constexpr int SMEM_BYTES = SMEM_STAGE + 8 * 2048 + 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 };
 constexpr int kChunkRows = 256;
@@ -117,6 +118,7 @@ struct Kv4ChunkWalk {
   const Kv4AttnParams& p;
   int R;
   long long u, u_end, first;                         // first: first tile of (b, qp)
+  long long mine0;                                   // tiles of the lane's (b, qp) entries, from total()
   int b, qp, h, len, n, kt0, kt1, nkv, lim_all;
   int end[2];
 
@@ -134,6 +136,7 @@ struct Kv4ChunkWalk {
   __device__ __forceinline__ long long total(int lane) {
     long long s = 0;
     for (int i = lane; i < p.c.B * p.row_blocks; i += 32) s += tiles(i);
+    mine0 = s * p.c.H;
     return warp_sum(s) * p.c.H;
   }
   // to the run [u0, u1) (the whole warp takes part)
@@ -142,7 +145,8 @@ struct Kv4ChunkWalk {
     u_end = u1;
     first = 0;
     for (int i0 = 0;; i0 += 32) {
-      const long long mine = i0 + lane < p.c.B * p.row_blocks ? static_cast<long long>(tiles(i0 + lane)) * p.c.H : 0;
+      const long long mine = p.c.B * p.row_blocks <= 32 ? mine0
+                             : i0 + lane < p.c.B * p.row_blocks ? static_cast<long long>(tiles(i0 + lane)) * p.c.H : 0;
       long long incl = mine;
 #pragma unroll
       for (int s = 1; s < 32; s <<= 1) {
@@ -421,7 +425,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         if (lane == 0) {
           Kv4Seg x;
           x.kt0 = over ? 0 : w.kt0, x.kt1 = over ? 0 : w.kt1;
-          x.end[0] = w.end[0], x.end[1] = w.end[1];
+          x.end[0] = over ? 0 : w.end[0], x.end[1] = over ? 0 : w.end[1];
           x.len = w.len, x.n = w.n;
           x.r0 = w.qp * kChunkRows;
           x.slot = !over && w.whole() ? -1 : 2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1);
@@ -580,8 +584,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
     const uint32_t o_tm = tmem_base + lane_off + C::O_COL0 + t * D;
     uint32_t sc = 0, oc = 0;                          // phases of s_full and o_done
     const int R = p.Hq / p.c.H * p.N;
-    // The warp's 32 rows of its tile's q also stage its output: row i holds UPR 16-byte units, RPI rows
-    // make 32 of them.
+    // A row of q or of 16-bit output is UPR 16-byte units; RPI rows make 32 of them.
     constexpr int UPR = D / 8, RPI = 32 / UPR;
     // (the thread's place is read anew, opaquely, where a segment begins and ends: what is derived from it
     // would otherwise be kept in registers through the tile loop, which spills for it)
@@ -590,9 +593,31 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
       asm volatile("mov.u32 %0, %%tid.x;" : "=r"(x));
       return static_cast<int>(x);
     };
+    // Copies the q rows of segment sg to the warp's rows of this group's q tile, whole rows to consecutive
+    // lanes (zeros behind the last row). The tile is free: every S MMA that read it has completed when
+    // this group has seen its last S. PAIR: group 1 fills the second tile's place with the same rows for
+    // itself; the MMA reads group 0's.
+    auto copy_q = [&](uint32_t sg) {
+      volatile const Kv4Seg& w = segs[sg % C::RING];
+      const int here = thread_here(), ln = here & 31, w0 = (here & 127) & ~31, tile = here >> 7;
+      if (C::PAIR ? w.kt0 + tile < w.kt1 : w.kt0 < w.end[tile]) {
+        const int row0 = w.r0 + (C::PAIR ? 0 : tile * 128) + w0;
+        const uint8_t* src = p.q + (w.row + row0) * (D * 2) + (ln % UPR) * 16;
+        const uint32_t dst = smem_addr(smem + C::SMEM_Q + tile * C::TILE_BYTES) + ((ln % UPR) >> 3) * C::CHUNK_BYTES;
+#pragma unroll 1   // (unrolled, ptxas schedules the tile loop worse: 1.12 against 1.04 ms)
+        for (int it = 0; it < UPR; ++it) {
+          const int i = it * RPI + ln / UPR, rw = w0 + i;
+          const bool valid = row0 + i < R;
+          cp_async_16z(dst + rw * 128 + ((((ln % UPR) & 7) ^ (rw & 7)) << 4), valid ? src + static_cast<size_t>(i) * D * 2 : p.q,
+                       valid);
+        }
+      }
+      cp_async_commit();
+    };
     uint32_t xc = 0;                                  // PAIR: segments so far (phases of xch_full, xch_empty)
     float2* xch = reinterpret_cast<float2*>(smem + C::SMEM_XCH);
-    for (uint32_t sg = 0; ok && (ok = take_segment(sg)); ++sg) {
+    if ((ok = take_segment(0))) copy_q(0);
+    for (uint32_t sg = 0; ok; ++sg) {
       // (read again after the tile loop, which has no registers to spare for the segment's fields)
       volatile const Kv4Seg& w = segs[sg % C::RING];
       const int j0 = w.kt0 + (C::PAIR ? t : 0), endt = C::PAIR ? w.kt1 : w.end[t];   // this group's key tiles:
@@ -606,64 +631,49 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         if (!C::PAIR && endt <= j0) {
           if (w.slot >= 0) p.part_ml[static_cast<size_t>(w.slot) * kChunkRows + tile_row] = make_float2(-INFINITY, 0.f);
           free_segment(sg);
+          if ((ok = take_segment(sg + 1))) copy_q(sg + 1);
           continue;
         }
       }
-      // ---- q: every row scaled by a power of two, f16, into the tile's swizzled rows. The warp loads its
-      // 32 rows together (whole rows to consecutive lanes: a thread reading its own row would touch 32
-      // lines per load). Every S MMA that read the previous q has completed: this warp saw the last one's
-      // barrier (or, for group 1's, group 1's result). PAIR: group 0 writes it for both.
+      // ---- q has been copied (see copy_q); each row is scaled by a power of two and becomes f16 in
+      // place, a thread per row. PAIR: group 0 does it for both, group 1 only needs the factor.
       float c = 1.f;
       if (j0 < endt) {
-        const int here = thread_here(), lane = here & 31, wq = (here >> 5) & 3, ta = C::PAIR ? 0 : here >> 7;
-        uint8_t* const tile_rows = smem + C::SMEM_Q + ta * C::TILE_BYTES + wq * 32 * 128;
-        auto unit_at = [&](int i, int u) {
-          return tile_rows + (u >> 3) * C::CHUNK_BYTES + i * 128 + (((u & 7) ^ (i & 7)) << 4);
+        cp_async_wait<0>();
+        __syncwarp();
+        const int here = thread_here(), row = here & 127;
+        uint8_t* const tile_rows = smem + C::SMEM_Q + (here >> 7) * C::TILE_BYTES;
+        auto unit = [&](int u) {
+          return reinterpret_cast<uint4*>(tile_rows + (u >> 3) * C::CHUNK_BYTES + row * 128 + (((u & 7) ^ (row & 7)) << 4));
         };
-        const int row0 = w.r0 + ta * 128 + wq * 32;   // the warp's first row in (b, h), and in q
-        const unsigned long long qrow0 = w.row + row0;
-        int e_mine = 127;
-#pragma unroll 1
-        for (int it0 = 0; it0 < UPR; it0 += 8) {
-          uint4 x[8];                                 // (in flight together; the loop over them is not unrolled,
-#pragma unroll                                        // which cost the tile loop registers: 1.13 against 1.05 ms)
-          for (int k = 0; k < 8; ++k) {
-            const int i = (it0 + k) * RPI + lane / UPR;                  // row of the warp
-            x[k] = row0 + i < R ? __ldg(reinterpret_cast<const uint4*>(p.q) + (qrow0 + i) * UPR + lane % UPR)
-                                : make_uint4(0u, 0u, 0u, 0u);
-          }
-#pragma unroll 1
-          for (int k = 0; k < 8; ++k) {
-            const int it = it0 + k;
-            uint32_t xs[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
+        float amax = 0.f;
+#pragma unroll 4
+        for (int u = 0; u < D / 8; ++u) {
+          const uint4 x = *unit(u);
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int s = 1; s < 8; ++s) x[s - 1] = x[s];
-            float amax = 0.f;
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = f32x2_from_16<F16>(xs[e]);
+            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+        const int e2 = kv4_row_exp(amax);
+        c = fmaxf(__int_as_float(e2 << 23) * p.scale_log2, 1e-37f);
+        if (!C::PAIR || t == 0) {
+          const float down = __int_as_float((254 - e2) << 23);
+#pragma unroll 4
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 x = *unit(u);
+            uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float2 f = f32x2_from_16<F16>(xs[e]);
-              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+              xs[e] = pack_f16x2(f.x * down, f.y * down);
             }
-#pragma unroll
-            for (int sft = 1; sft < UPR; sft <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, sft));
-            const int e2 = kv4_row_exp(amax);
-            const int got = __shfl_sync(0xffffffffu, e2, (lane % RPI) * UPR);
-            if (lane / RPI == it) e_mine = got;
-            if (!C::PAIR || t == 0) {
-              const float down = __int_as_float((254 - e2) << 23);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 f = f32x2_from_16<F16>(xs[e]);
-                xs[e] = pack_f16x2(f.x * down, f.y * down);
-              }
-              *reinterpret_cast<uint4*>(unit_at(it * RPI + lane / UPR, lane % UPR)) = make_uint4(xs[0], xs[1], xs[2], xs[3]);
-            }
+            *unit(u) = make_uint4(xs[0], xs[1], xs[2], xs[3]);
           }
-        }
-        c = fmaxf(__int_as_float(e_mine << 23) * p.scale_log2, 1e-37f);
-        if (!C::PAIR || t == 0) {
           fence_proxy_async_shared();
-          mbar_arrive(q_full + ta);
+          mbar_arrive(q_full + (C::PAIR ? 0 : t));
         }
       }
       float m_run = -INFINITY, l_run = 0.f;
@@ -705,6 +715,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         m_run = m_use;
       }
       if (!ok) break;
+      // the next segment's q comes in under this one's last P V and its output (PAIR: group 1's S MMAs
+      // read group 0's tile too, so that group 0 copies once group 1's result is complete)
+      if (!(ok = take_segment(sg + 1))) break;
+      if (!C::PAIR || t == 1) copy_q(sg + 1);
       if (!C::PAIR || j0 < endt) {
         if (!(ok = wait_all(o_done + t, oc & 1))) break;
         ++oc;
@@ -712,10 +726,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
       }
       const int here = thread_here(), lane = here & 31, wq = (here >> 5) & 3, ta = C::PAIR ? 0 : here >> 7;
       const int r = wq * 32 + lane;
-      uint8_t* const tile_rows = smem + C::SMEM_Q + ta * C::TILE_BYTES + wq * 32 * 128;
-      auto unit_at = [&](int i, int u) {
-        return tile_rows + (u >> 3) * C::CHUNK_BYTES + i * 128 + (((u & 7) ^ (i & 7)) << 4);
-      };
+      // output rows pass through shared memory, 64 bytes of each of the warp's 32 at a time, so that
+      // consecutive lanes write whole sectors of a row
+      uint8_t* const stage = smem + C::SMEM_STAGE + (here >> 5) * 2048;
+      auto unit_at = [&](int i, int u) { return reinterpret_cast<uint4*>(stage + i * 64 + ((u ^ ((i >> 1) & 3)) << 4)); };
       const bool whole = w.slot < 0;
       const int row0 = w.r0 + ta * 128 + wq * 32;
       const unsigned long long qrow0 = w.row + row0;
@@ -736,6 +750,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         }
         if (!(ok = wait_all(xch_full, ph))) break;
         tc_fence_after();
+        copy_q(sg + 1);
         const float2 x = xch[r];
         const float M = fmaxf(m_run, x.x), Mu = M == -INFINITY ? 0.f : M;
         f0 = ex2_approx(m_run - Mu);
@@ -749,11 +764,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         f1 *= inv;
       }
       const bool join = C::PAIR && w.kt1 - w.kt0 > 1; // group 1 had a tile
-      // O leaves through the warp's rows of the q tile (its S MMAs are complete), so that whole rows go to
-      // consecutive lanes: 16 bits in one turn, fp32 parts half a row at a time
       const uint32_t wmask = __ballot_sync(0xffffffffu, write);
       uint8_t* const gout = whole ? p.o + qrow0 * D * 2
                                   : reinterpret_cast<uint8_t*>(p.part_o + (prow - lane) * static_cast<size_t>(D));
+      // the staged 64 bytes of every row to bytes [at, at + 64) of its row of `bytes` bytes
+      auto flush = [&](int bytes, int at) {
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const int i = it * 8 + lane / 4;
+          const uint4 x = *unit_at(i, lane & 3);
+          if (!whole || ((wmask >> i) & 1u))
+            *reinterpret_cast<uint4*>(gout + static_cast<size_t>(i) * bytes + at + (lane & 3) * 16) = x;
+        }
+        __syncwarp();
+      };
 #pragma unroll
       for (int cb = 0; cb < D; cb += 32) {
         uint32_t ov[32];
@@ -778,26 +803,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               pk[e] = pack_16<F16>(__uint_as_float(ov[8 * i + 2 * e]), __uint_as_float(ov[8 * i + 2 * e + 1]));
-            *reinterpret_cast<uint4*>(unit_at(lane, cb / 8 + i)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *unit_at(lane, i) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
+          flush(D * 2, cb * 2);
         } else {
-          const int cu = (cb % (D / 2)) / 4;          // first unit of these columns in their half
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint4*>(unit_at(lane, cu + i)) =
-                make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
-        }
-        if (whole ? cb + 32 == D : (cb + 32) % (D / 2) == 0) {
-          __syncwarp();
-          const int bytes = whole ? D * 2 : D * 4, first = whole ? 0 : (cb / (D / 2)) * D * 2;
-#pragma unroll 4
-          for (int it = 0; it < UPR; ++it) {
-            const int i = it * RPI + lane / UPR;
-            const uint4 x = *reinterpret_cast<const uint4*>(unit_at(i, lane % UPR));
-            if (!whole || ((wmask >> i) & 1u))
-              *reinterpret_cast<uint4*>(gout + static_cast<size_t>(i) * bytes + first + (lane % UPR) * 16) = x;
+          for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *unit_at(lane, i) = make_uint4(ov[16 * hf + 4 * i], ov[16 * hf + 4 * i + 1], ov[16 * hf + 4 * i + 2],
+                                             ov[16 * hf + 4 * i + 3]);
+            flush(D * 4, cb * 4 + 64 * hf);
           }
-          __syncwarp();
         }
       }
       if constexpr (C::PAIR) {
@@ -809,6 +826,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         p.lse[qrow0 + lane] = l_run == 0.f ? -INFINITY : (m_run + __log2f(l_run)) * 0.69314718055994531f;
       free_segment(sg);
     }
+    cp_async_wait<0>();
     if (!ok) record_timeout();
   }
 
