@@ -593,56 +593,70 @@ class KV4Cache:
         return cls(*new, k_exp=k_exp, v_exp=v_exp)
 
 
-def _kv4_int32(t, name, shape, device):
+def _kv4_int32(t, name, size, device):
     import torch
-    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+    if t.dtype is not torch.int32 or t.shape != size or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(size)} on {device}")
     return t.data_ptr()
 
 
 def _kv4_rows(t, name, cache, heads=None):
     """Sizes and element type of a 16-bit [B, H, N, d] argument of the cache calls."""
     import torch
-    if t.dim() != 4 or not t.is_contiguous() or t.device != cache.device or \
-            (t.dtype is not torch.bfloat16 and t.dtype is not torch.float16):
+    dt = t.dtype
+    shape = t.shape
+    if len(shape) != 4 or t.device != cache.device or not t.is_contiguous() or \
+            (dt is not torch.bfloat16 and dt is not torch.float16):
         raise ValueError(f"{name} must be a contiguous bf16 or fp16 tensor [B, H, N, d] on {cache.device}")
-    B, H, N, d = t.shape
+    B, H, N, d = shape
     if d != cache.d or (heads is not None and H != heads):
         raise ValueError(f"{name} has {H} heads of width {d}: the cache has {cache.heads} of {cache.d}")
-    return B, H, N, ATTN_BF16 if t.dtype is torch.bfloat16 else ATTN_FP16
+    return B, H, N, ATTN_BF16 if dt is torch.bfloat16 else ATTN_FP16
+
+
+def _kv4_like(t, name, ref):
+    """A tensor argument that must be like `ref`."""
+    if t.shape != ref.shape or t.dtype is not ref.dtype or t.device != ref.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {ref.dtype} tensor of shape {tuple(ref.shape)} on {ref.device}")
 
 
 def _kv4_tables(cache, block_table, seq_lens, B):
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B:
         raise ValueError(f"block_table must be int32 [{B}, max_pages]")
-    return _kv4_int32(block_table, "block_table", block_table.shape, cache.device), \
-        _kv4_int32(seq_lens, "seq_lens", (B,), cache.device)
+    return _kv4_int32(block_table, "block_table", shape, cache.device), \
+        _kv4_int32(seq_lens, "seq_lens", (B,), cache.device), shape[1]
 
 
 class _kv4_place:
     """Runs a launch with the tensors' device current and, for torch allocations, the
     launch's stream current (a buffer made here then belongs to that stream)."""
 
-    __slots__ = ("device", "stream", "ctx")
+    __slots__ = ("ctx", "sp")
 
     def __init__(self, device, stream):
-        self.device, self.stream, self.ctx = device, stream, ()
-
-    def __enter__(self):
         import torch
-        index = self.device.index
-        if self.stream is None and index == torch._C._cuda_getDevice():
-            return torch._C._cuda_getCurrentRawStream(index)
-        self.ctx = [torch.cuda.device(self.device)]
-        if self.stream is not None:
-            self.ctx.append(torch.cuda.stream(self.stream))
+        self.ctx = [torch.cuda.device(device)]
+        if stream is not None:
+            self.ctx.append(torch.cuda.stream(stream))
         for c in self.ctx:
             c.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+        self.sp = torch.cuda.current_stream(device).cuda_stream
 
-    def __exit__(self, *exc):
+    def leave(self):
         for c in reversed(self.ctx):
-            c.__exit__(*exc)
+            c.__exit__(None, None, None)
+
+
+def _kv4_stream(cache, stream):
+    """(raw stream, place to leave or None): nothing to switch in the usual case, the
+    current stream of the current device."""
+    import torch
+    index = cache.device.index
+    if stream is None and index == torch._C._cuda_getDevice():
+        return torch._C._cuda_getCurrentRawStream(index), None
+    place = _kv4_place(cache.device, stream)
+    return place.sp, place
 
 
 def kv4_append(cache, k, v, block_table, seq_lens, new_lens=None, stream=None, check=False):
@@ -653,16 +667,20 @@ def kv4_append(cache, k, v, block_table, seq_lens, new_lens=None, stream=None, c
     block_table[b, position // page_size]. Asynchronous; a page number or length outside
     the cache skips the write and is reported by attn_get_device_status()
     (check=True waits and raises). Returns the cache."""
-    B, _, N, dt = _kv4_rows(k, "k", cache, cache.heads)
-    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device or not v.is_contiguous():
-        raise ValueError("v must be a contiguous tensor like k")
-    bt, sl = _kv4_tables(cache, block_table, seq_lens, B)
+    B, H, N, dt = _kv4_rows(k, "k", cache, cache.heads)
+    _kv4_like(v, "v", k)
+    bt, sl, max_pages = _kv4_tables(cache, block_table, seq_lens, B)
     nl = None if new_lens is None else _kv4_int32(new_lens, "new_lens", (B,), cache.device)
-    with _kv4_place(cache.device, stream) as sp:
-        _check(attn_kv4_append(k.data_ptr(), v.data_ptr(), *cache._ptrs, bt, sl, nl, B, cache.heads, N, cache.d,
-                               cache.num_pages, cache.page_size, block_table.shape[1], cache.k_exp, cache.v_exp, dt,
-                               sp), "attn_kv4_append")
-        _check_device(check, sp, "attn_kv4_append")
+    sp, place = _kv4_stream(cache, stream)
+    try:
+        _check(attn_kv4_append(k.data_ptr(), v.data_ptr(), *cache._ptrs, bt, sl, nl, B, H, N, cache.d,
+                               cache.num_pages, cache.page_size, max_pages, cache.k_exp, cache.v_exp, dt, sp),
+               "attn_kv4_append")
+        if check:
+            _check_device(check, sp, "attn_kv4_append")
+    finally:
+        if place is not None:
+            place.leave()
     return cache
 
 
@@ -672,22 +690,44 @@ def kv4_read(cache, block_table, seq_lens, N, starts=None, dtype=None, k=None, v
     bad page numbers and lengths as in kv4_append."""
     import torch
     B = seq_lens.shape[0]
-    bt, sl = _kv4_tables(cache, block_table, seq_lens, B)
+    bt, sl, max_pages = _kv4_tables(cache, block_table, seq_lens, B)
     st = None if starts is None else _kv4_int32(starts, "starts", (B,), cache.device)
-    shape = (B, cache.heads, int(N), cache.d)
-    with _kv4_place(cache.device, stream) as sp:
+    sp, place = _kv4_stream(cache, stream)
+    try:
         if k is None:
-            k = torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=cache.device)
+            k = torch.empty((B, cache.heads, N, cache.d), dtype=torch.bfloat16 if dtype is None else dtype,
+                            device=cache.device)
+        kB, H, kN, dt = _kv4_rows(k, "k", cache, cache.heads)
+        if kB != B or kN != N or (dtype is not None and k.dtype is not dtype):
+            raise ValueError(f"k must be [{B}, {H}, {N}, {cache.d}]" + ("" if dtype is None else f" of {dtype}"))
         if v is None:
-            v = torch.empty(shape, dtype=k.dtype, device=cache.device)
-        dt = _kv4_rows(k, "k", cache, cache.heads)[3]
-        for name, t in (("k", k), ("v", v)):
-            _expect(t, name, shape, k.dtype if dtype is None else dtype, cache.device)
-        _check(attn_kv4_read(*cache._ptrs, bt, sl, st, k.data_ptr(), v.data_ptr(), B, cache.heads, int(N), cache.d,
-                             cache.num_pages, cache.page_size, block_table.shape[1], cache.k_exp, cache.v_exp, dt,
-                             sp), "attn_kv4_read")
-        _check_device(check, sp, "attn_kv4_read")
+            v = torch.empty_like(k)
+        _kv4_like(v, "v", k)
+        _check(attn_kv4_read(*cache._ptrs, bt, sl, st, k.data_ptr(), v.data_ptr(), B, H, N, cache.d, cache.num_pages,
+                             cache.page_size, max_pages, cache.k_exp, cache.v_exp, dt, sp), "attn_kv4_read")
+        if check:
+            _check_device(check, sp, "attn_kv4_read")
+    finally:
+        if place is not None:
+            place.leave()
     return k, v
+
+
+# workspaces of forward_kv4, one per (device, stream): launches of one stream run in order
+_KV4_WORKSPACES = {}
+
+
+def _kv4_workspace(device, sp, need):
+    import torch
+    if torch._C._cuda_isCurrentStreamCapturing():
+        # a graph has its own: it may be replayed on any stream, next to any other call
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    key = (device.index, sp)
+    ws = _KV4_WORKSPACES.get(key)
+    if ws is None or ws.shape[0] < need:
+        # (made with that stream current: the memory of the old one goes back to its pool)
+        ws = _KV4_WORKSPACES[key] = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws
 
 
 def forward_kv4(q, cache, block_table, seq_lens, q_lens=None, causal=False, scale=None, out=None, lse=None,
@@ -700,40 +740,46 @@ def forward_kv4(q, cache, block_table, seq_lens, q_lens=None, causal=False, scal
     seq_lens); it sees every cached position, with causal=True only those up to its
     own. N = 1 is a decoding step. Rows behind q_lens[b] are left as they were in out
     and lse (zero where those are allocated here); a row that sees no key gets O = 0,
-    LSE = -inf. The workspace is allocated with torch unless given (see
-    attn_fwd_kv4_workspace_bytes). Asynchronous like forward(); bad page numbers and
-    lengths as in kv4_append."""
+    LSE = -inf. `workspace`: a uint8 tensor of at least attn_fwd_kv4_workspace_bytes(...);
+    None: one kept per device and stream (inside a graph capture: the graph's own).
+    Asynchronous like forward(); bad page numbers and lengths as in kv4_append."""
     import torch
     B, Hq, N, dt = _kv4_rows(q, "q", cache)
-    bt, sl = _kv4_tables(cache, block_table, seq_lens, B)
+    bt, sl, max_pages = _kv4_tables(cache, block_table, seq_lens, B)
     ql = None if q_lens is None else _kv4_int32(q_lens, "q_lens", (B,), cache.device)
-    with _kv4_place(cache.device, stream) as sp:
-        new = torch.empty if q_lens is None else torch.zeros
+    sp, place = _kv4_stream(cache, stream)
+    try:
         if out is None:
-            out = new(q.shape, dtype=q.dtype, device=q.device)
-        _expect(out, "out", q.shape, q.dtype, q.device)
-        if lse is None and with_lse:
-            lse = new((B, Hq, N), dtype=torch.float32, device=q.device)
-        if lse is not None:
+            out = (torch.empty if q_lens is None else torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            _kv4_like(out, "out", q)
+        if lse is None:
+            if with_lse:
+                lse = (torch.empty if q_lens is None else torch.zeros)((B, Hq, N), dtype=torch.float32, device=q.device)
+        else:
             _expect(lse, "lse", (B, Hq, N), torch.float32, q.device)
-        max_pages = block_table.shape[1]
         sizes = (B, Hq, N, max_pages)
         need = cache._need.get(sizes)
         if need is None:
-            need = attn_fwd_kv4_workspace_bytes(B, Hq, cache.heads, N, cache.d, cache.page_size, max_pages)
-            cache._need[sizes] = need
+            need = cache._need[sizes] = attn_fwd_kv4_workspace_bytes(B, Hq, cache.heads, N, cache.d, cache.page_size,
+                                                                     max_pages)
         if workspace is None:
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        elif workspace.device != q.device or not workspace.is_contiguous() or \
-                workspace.numel() * workspace.element_size() < need:
-            raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {q.device}")
-        _check(attn_fwd_kv4(q.data_ptr(), *cache._ptrs, bt, sl, ql, out.data_ptr(), _ptr(lse), _ptr(workspace),
-                            0 if workspace is None else workspace.numel() * workspace.element_size(), B, Hq,
-                            cache.heads, N, cache.d, cache.num_pages, cache.page_size, max_pages, cache.k_exp,
-                            cache.v_exp, 0.0 if scale is None else float(scale), int(bool(causal)), dt, sp),
-               "attn_fwd_kv4")
-        _check_device(check, sp, "attn_fwd_kv4")
+            # (a shape the library refuses needs none: the call below says why)
+            workspace = _kv4_workspace(q.device, sp, need) if need else None
+        elif workspace.device != q.device or workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or \
+                workspace.numel() < need:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {q.device}")
+        _check(attn_fwd_kv4(q.data_ptr(), *cache._ptrs, bt, sl, ql, out.data_ptr(),
+                            None if lse is None else lse.data_ptr(),
+                            None if workspace is None else workspace.data_ptr(),
+                            0 if workspace is None else workspace.numel(), B, Hq, cache.heads, N, cache.d,
+                            cache.num_pages, cache.page_size, max_pages, cache.k_exp, cache.v_exp,
+                            0.0 if scale is None else float(scale), 1 if causal else 0, dt, sp), "attn_fwd_kv4")
+        if check:
+            _check_device(check, sp, "attn_fwd_kv4")
+    finally:
+        if place is not None:
+            place.leave()
     return out, lse
 
 

@@ -149,7 +149,7 @@ int sm_count() {
 // belongs to the function on the current device; later calls skip the driver
 // call). `tag` identifies the kernel. A failed launch forgets the flag, so a
 // context that was reset gets the attribute again on the next call.
-constexpr int kSmemTags = 40;
+constexpr int kSmemTags = 32;
 std::atomic<uint32_t> g_smem_done[64][kSmemTags];
 
 void forget_smem(int tag) {

@@ -64,14 +64,15 @@ struct Kv4Plan {
   size_t ml_bytes, o_bytes, workspace;
 };
 constexpr int kKv4Sms = 148;
-#ifndef KV4_CHUNK_ROWS
-#define KV4_CHUNK_ROWS 32
-#endif
+// Rows up to which the decode kernel runs (blocks of 8 or 16 rows). A (b, cached head) of 32 rows over
+// 8 sequences of about 6000 keys and 4 heads: 30.9 us in two blocks of 16, 56.5 in the chunk kernel; of 48 rows 48.9
+// in the chunk kernel and a third block's 15 us more here.
+constexpr int kKv4DecodeRows = 32;
 
 Kv4Plan kv4_plan(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {
   Kv4Plan r;
   const long long rows = static_cast<long long>(Hq / Hkv) * N;
-  r.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : (rows <= KV4_CHUNK_ROWS ? 4 : 0));
+  r.nt = rows <= 8 ? 1 : (rows <= kKv4DecodeRows ? 2 : 0);
   const int block = r.nt > 0 ? 8 * r.nt : attn::kChunkRows, keys = r.nt > 0 ? attn::kDecTile : 128;
   r.row_blocks = static_cast<int>((rows + block - 1) / block);
   const long long tiles = (static_cast<long long>(max_pages) * page_size + keys - 1) / keys;
@@ -80,7 +81,7 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pa
   r.ctas = static_cast<int>(units < most ? units : most);
   r.ml_bytes = static_cast<size_t>(2) * r.ctas * block * sizeof(float2);
   r.o_bytes = static_cast<size_t>(2) * r.ctas * block * d * sizeof(float);
-  r.workspace = r.ml_bytes + r.o_bytes + (r.nt > 0 ? 0 : (r.ctas * sizeof(attn::Kv4Head) + 15) / 16 * 16);
+  r.workspace = r.ml_bytes + r.o_bytes + (r.ctas * sizeof(attn::Kv4Head) + 15) / 16 * 16;
   return r;
 }
 
@@ -105,8 +106,7 @@ attn_status launch_kv4_dec(const attn::Kv4AttnParams& p, int tag, cudaStream_t s
   auto kern = attn::kv4_decode_sm100<C, F16>;
   if (!set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, tag)) return ATTN_ERR_CUDA;
   kern<<<p.ctas, attn::kDecWarps * 32, C::SMEM_BYTES, stream>>>(p);
-  const cudaError_t e = launch_after(attn::kv4_combine_sm100<C, F16>,
-                                     dim3(static_cast<unsigned>(p.c.B * p.Hq * p.N)), 128, stream, p);
+  const cudaError_t e = launch_after(attn::kv4_join_sm100<C::D, C::ROWS, F16>, dim3(p.ctas, C::ROWS / 8), 256, stream, p);
   if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) {
     forget_smem(tag);
     return ATTN_ERR_CUDA;
@@ -115,16 +115,13 @@ attn_status launch_kv4_dec(const attn::Kv4AttnParams& p, int tag, cudaStream_t s
 }
 
 template <int D, bool F16, bool PAIR>
-attn_status launch_kv4_chunk(const attn::Kv4AttnParams& p, const Kv4Plan& plan, int tag, cudaStream_t stream) {
+attn_status launch_kv4_chunk(const attn::Kv4AttnParams& p, int tag, cudaStream_t stream) {
   using C = attn::Kv4ChunkCfg<D, PAIR>;
   auto kern = attn::kv4_chunk_sm100<C, F16>;
   if (!set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, tag)) return ATTN_ERR_CUDA;
-  attn::Kv4ChunkParams cp;
-  cp.a = p;
-  cp.heads = reinterpret_cast<attn::Kv4Head*>(reinterpret_cast<uint8_t*>(p.part_o) + plan.o_bytes);
-  cp.timeout_cycles = kWaitLimitCycles;
-  kern<<<p.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(cp);
-  const cudaError_t e = launch_after(attn::kv4_chunk_join_sm100<C, F16>, dim3(p.ctas, (PAIR ? 128 : attn::kChunkRows) / 8), 256, stream, cp);
+  kern<<<p.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(attn::Kv4ChunkParams{p, kWaitLimitCycles});
+  const cudaError_t e = launch_after(attn::kv4_join_sm100<D, attn::kChunkRows, F16>,
+                                     dim3(p.ctas, (PAIR ? 128 : attn::kChunkRows) / 8), 256, stream, p);
   if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) {
     forget_smem(tag);
     return ATTN_ERR_CUDA;
@@ -134,13 +131,12 @@ attn_status launch_kv4_chunk(const attn::Kv4AttnParams& p, const Kv4Plan& plan, 
 
 template <int D, bool F16>
 attn_status launch_kv4_rows(const attn::Kv4AttnParams& p, const Kv4Plan& plan, cudaStream_t stream) {
-  const int tag = 16 + (D == 128 ? 0 : 10) + (F16 ? 5 : 0);
+  const int tag = 16 + (D == 128 ? 0 : 8) + (F16 ? 4 : 0);
   if (plan.nt == 0)
-    return p.Hq / p.c.H * p.N <= 128 ? launch_kv4_chunk<D, F16, true>(p, plan, tag + 3, stream)
-                                     : launch_kv4_chunk<D, F16, false>(p, plan, tag + 4, stream);
+    return p.Hq / p.c.H * p.N <= 128 ? launch_kv4_chunk<D, F16, true>(p, tag + 2, stream)
+                                     : launch_kv4_chunk<D, F16, false>(p, tag + 3, stream);
   if (plan.nt == 1) return launch_kv4_dec<attn::Kv4DecCfg<D, 1>, F16>(p, tag, stream);
-  if (plan.nt == 2) return launch_kv4_dec<attn::Kv4DecCfg<D, 2>, F16>(p, tag + 1, stream);
-  return launch_kv4_dec<attn::Kv4DecCfg<D, 4>, F16>(p, tag + 2, stream);
+  return launch_kv4_dec<attn::Kv4DecCfg<D, 2>, F16>(p, tag + 1, stream);
 }
 
 }  // namespace
@@ -237,8 +233,10 @@ attn_status attn_fwd_kv4(const void* q, const void* k_codes, const void* k_sf, c
   const Kv4Plan plan = kv4_plan(B, Hq, Hkv, N, d, page_size, max_pages);
   p.row_blocks = plan.row_blocks;
   p.ctas = plan.ctas;
-  p.part_ml = static_cast<float2*>(workspace);
-  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.ml_bytes);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(ws);
+  p.part_o = reinterpret_cast<float*>(ws + plan.ml_bytes);
+  p.heads = reinterpret_cast<attn::Kv4Head*>(ws + plan.ml_bytes + plan.o_bytes);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (d == 128) return dtype == ATTN_FP16 ? launch_kv4_rows<128, true>(p, plan, st) : launch_kv4_rows<128, false>(p, plan, st);
   return dtype == ATTN_FP16 ? launch_kv4_rows<64, true>(p, plan, st) : launch_kv4_rows<64, false>(p, plan, st);

@@ -27,8 +27,11 @@
 // Schedule: the 256-key tiles of all (b, h, row block) make one long list that is cut into
 // equal runs, one per CTA, so uneven lengths balance without the host knowing them. A run
 // that covers part of a (b, h, row block) writes its unnormalised O, maximum and sum to the
-// workspace (two slots per CTA: a run's first and last item); kv4_combine_sm100 joins
-// them in the order of the CTAs, so results do not depend on timing.
+// workspace (two slots per CTA: a run's first and last item); kv4_join_sm100 joins the parts in
+// the order of the runs, so results do not depend on timing. It is launched with programmatic
+// serialisation, so that its launch hides under the main kernel. (A join by the CTA that takes the item's last
+// ticket instead, without a second kernel, was slower: its fence and atomic stand in every split
+// segment's way, 26.6 against 20.8 us on 16 sequences of up to 4096 keys x 8 heads.)
 //
 // Bound: HBM at 4.5 bits a value is 13e12 values / s; a value costs about half a conversion
 // and half a multiplication (64 lanes / clk / SM each).
@@ -57,11 +60,15 @@ struct Kv4DecCfg {
   static constexpr int O_LD = D + 8;               // floats between rows of a warp's O
   static_assert(8 * O_LD * 4 <= STAGE && STAGES >= NT + 2, "merge stages");
   static constexpr int SMEM_ML = RING;             // [warps][ROWS] (max, sum)
-  static constexpr bool QREG = NT <= 2;            // q fragments in registers, else in shared memory
   static constexpr int KSTEPS = D / 16;
-  static constexpr int SMEM_Q = SMEM_ML + kDecWarps * ROWS * 8;
-  static constexpr int SMEM_BYTES = SMEM_Q + (QREG ? 0 : KSTEPS * NT * 32 * 8);
+  static constexpr int SMEM_BYTES = SMEM_ML + kDecWarps * ROWS * 8;
   static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 233472, "shared memory per SM");
+};
+
+// An item's (a unit's) first part, as the CTA that wrote it leaves it for the join.
+struct Kv4Head {
+  int parts;                 // 0: this CTA has none
+  int b, h, rb, slot;        // rb: row block
 };
 
 struct Kv4AttnParams {
@@ -72,6 +79,7 @@ struct Kv4AttnParams {
   const int* q_lens;         // or nullptr
   float* part_o;             // workspace: [2 ctas][ROWS][D]
   float2* part_ml;           // [2 ctas][ROWS] (maximum in log2 units, sum)
+  Kv4Head* heads;            // [ctas]
   int Hq, N, causal;
   int row_blocks;            // ceil(Hq / Hkv * N / ROWS)
   int ctas;                  // CTAs of the main kernel (at most; see kv4_runs)
@@ -150,14 +158,41 @@ __device__ __forceinline__ int kv4_row_exp(float amax) {
   return ef == 255 ? 127 : max(ef, 10) - 9;
 }
 
+// O = 0, LSE = -infinity for the rows that see no key.
+template <int D>
+__device__ __forceinline__ void kv4_empty_rows(const Kv4AttnParams& p, int thread, int threads) {
+  for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
+    const int len = kv4_len(p.c, b), n = kv4_qlen(p, b);
+    const int z = len == 0 ? n : (p.causal ? max(0, n - len) : 0);
+    if (z == 0) continue;
+    constexpr int V4 = D / 8;                        // 16-byte pieces of a row
+    for (long long i = thread; i < static_cast<long long>(p.Hq) * z * V4; i += threads) {
+      const long long r = i / V4;
+      const size_t row = (static_cast<size_t>(b) * p.Hq + r / z) * p.N + r % z;
+      reinterpret_cast<uint4*>(p.o)[row * V4 + i % V4] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse != nullptr && i % V4 == 0) p.lse[row] = -INFINITY;
+    }
+  }
+}
+
+// One row's result from its unnormalised O (4 channels a lane at d4), maximum and sum.
+template <int D, bool F16>
+__device__ __forceinline__ void kv4_write_row(const Kv4AttnParams& p, size_t row, int d4, float4 a, float M, float L) {
+  const float inv = L == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / L;
+  reinterpret_cast<uint2*>(p.o)[row * (D / 4) + d4] =
+      make_uint2(pack_16<F16>(a.x * inv, a.y * inv), pack_16<F16>(a.z * inv, a.w * inv));
+  if (p.lse != nullptr && d4 == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+}
+
 template <class C, bool F16>
 __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm100(const Kv4AttnParams p) {
   constexpr int D = C::D, NT = C::NT, ROWS = C::ROWS;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const uint32_t smem0 = b200::smem_addr(smem_raw);
-  const uint32_t ring = smem0 + warp * C::STAGES * C::STAGE;
   asm volatile("griddepcontrol.launch_dependents;");
+  if (tid == 0) p.heads[blockIdx.x].parts = 0;
+  const uint32_t ring = smem0 + warp * C::STAGES * C::STAGE;
 
   // Copies. Codes: lane takes bytes [16 lane, 16 lane + 16) of every 512 of a group's. Scales: lane
   // takes 16 bytes of (tensor, group, piece); `grp` is also the group whose page it looks up.
@@ -187,7 +222,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
   }
   const long long my_units = total * per_b;
   const Kv4Runs runs(warp_sum(my_units), p.ctas);
-  if (static_cast<int>(blockIdx.x) >= runs.n) return;
+  if (static_cast<int>(blockIdx.x) >= runs.n) {
+    kv4_empty_rows<D>(p, tid, kDecWarps * 32);
+    return;
+  }
   long long u = runs.start(blockIdx.x);
   const long long u_begin = u, u_end = runs.start(blockIdx.x + 1);
   int b = 0;
@@ -320,7 +358,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
   if (AHEAD) load_q(0);
   for (;;) {
     // ---- q fragments
-    uint32_t qf[C::QREG ? NT : 1][C::KSTEPS][2];
+    uint32_t qf[NT][C::KSTEPS][2];
     float cs[NT][2], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -343,13 +381,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
       }
 #pragma unroll
       for (int k = 0; k < C::KSTEPS; ++k) {
-        if constexpr (C::QREG) {
-          qf[nt][k][0] = w[2 * k];
-          qf[nt][k][1] = w[2 * k + 1];
-        } else if (warp == nt % kDecWarps) {
-          *reinterpret_cast<uint2*>(smem_raw + C::SMEM_Q + ((k * NT + nt) * 32 + lane) * 8) =
-              make_uint2(w[2 * k], w[2 * k + 1]);
-        }
+        qf[nt][k][0] = w[2 * k];
+        qf[nt][k][1] = w[2 * k + 1];
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -359,7 +392,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
         l[nt][j] = 0.f;
       }
     }
-    if constexpr (!C::QREG) __syncthreads();
     const int lim_all = p.causal ? len - n : len - 1;       // every row sees the keys up to here
     float o[NT][D / 16][4];
 #pragma unroll
@@ -415,12 +447,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
             const int k = 2 * wd + hf;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint2 qq = C::QREG ? make_uint2(qf[C::QREG ? nt : 0][k][0], qf[C::QREG ? nt : 0][k][1])
-                                       : *reinterpret_cast<const uint2*>(smem_raw + C::SMEM_Q + ((k * NT + nt) * 32 + lane) * 8);
               if (k == 0)
-                mma_16816_zero(s[mt][nt], a, qq.x, qq.y);
+                mma_16816_zero(s[mt][nt], a, qf[nt][k][0], qf[nt][k][1]);
               else
-                mma_16816(s[mt][nt], a, qq.x, qq.y);
+                mma_16816(s[mt][nt], a, qf[nt][k][0], qf[nt][k][1]);
             }
           }
         }
@@ -554,6 +584,12 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
     const bool whole = t0 == 0 && t1 == T;
     const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
     const int out_rb = rb, out_n = n;
+    if (tid == 0 && t0 == 0 && !whole) {            // the item's first part: what the join needs
+      Kv4Head hd;
+      hd.parts = runs.cta_of(item_first + T - 1) - static_cast<int>(blockIdx.x) + 1;
+      hd.b = b, hd.h = h, hd.rb = rb, hd.slot = slot;
+      p.heads[blockIdx.x] = hd;
+    }
     const size_t out_row0 = row0;
     u = item_first + t1;
     wr = rd;
@@ -612,92 +648,71 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
       if (whole) {
         const int rr = out_rb * ROWS + r;
         if (rr < R && rr % p.N < out_n) {
-          const float inv = L == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / L;
-          reinterpret_cast<uint2*>(p.o)[(out_row0 + rr) * V4 + d4] =
-              make_uint2(pack_16<F16>(a.x * inv, a.y * inv), pack_16<F16>(a.z * inv, a.w * inv));
-          if (p.lse != nullptr && d4 == 0)
-            p.lse[out_row0 + rr] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+          kv4_write_row<D, F16>(p, out_row0 + rr, d4, a, M, L);
         }
       } else {
         reinterpret_cast<float4*>(p.part_o)[(static_cast<size_t>(slot) * ROWS + r) * V4 + d4] = a;
         if (d4 == 0) p.part_ml[static_cast<size_t>(slot) * ROWS + r] = make_float2(M, L);
       }
     }
-    if (!more) return;
+    if (!more) break;
     __syncthreads();
     if constexpr (NT > 1) issue_next(NT - 1);
   }
+  kv4_empty_rows<D>(p, tid, kDecWarps * 32);
 }
 
-// Joins the parts of the (b, h, row block) that several runs share, and writes the rows of
-// sequences without keys. One CTA of 128 threads per row: its four warps take every fourth
-// part, a lane 4 channels (D = 128; two lanes' worth idle at D = 64).
-template <class C, bool F16>
-__global__ void __launch_bounds__(128) kv4_combine_sm100(const Kv4AttnParams p) {
-  constexpr int D = C::D, ROWS = C::ROWS, V4 = D / 4;
-  __shared__ float4 so[4][V4];
-  __shared__ float2 sml[4];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int R = p.Hq / p.c.H * p.N;
-  const int rr = blockIdx.x % R, bh = blockIdx.x / R;
-  const int b = bh / p.c.H, h = bh % p.c.H, rb = rr / ROWS, r = rr % ROWS;
-  const int n = kv4_qlen(p, b);
-  const int per_b = p.c.H * p.row_blocks;
-  long long total = 0, before = 0;
-  for (int i = lane; i < p.c.B; i += 32) {
-    const int T = kv4_tiles(p, i);
-    total += T;
-    if (i < b) before += T;
-  }
-  const Kv4Runs runs(warp_sum(total) * per_b, p.ctas);
-  const int T = kv4_tiles(p, b);
-  const size_t row = static_cast<size_t>(bh) * R + rr;
-  // every CTA waits, so that this grid ends after the main one whatever it has to do
+// Joins the parts of the item whose first part CTA blockIdx.x wrote (row blocks of ROWS rows): a warp per
+// row. A lane holds the
+// (maximum, sum) of one part, so that the parts' O, D / 32 channels a lane, load without waiting for
+// one another.
+template <int D, int ROWS, bool F16>
+__global__ void __launch_bounds__(256) kv4_join_sm100(const Kv4AttnParams p) {
+  constexpr int E = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (rr % p.N >= n) return;
-  if (T == 0) {
-    if (warp == 0 && lane < V4) reinterpret_cast<uint2*>(p.o)[row * V4 + lane] = make_uint2(0u, 0u);
-    if (p.lse != nullptr && tid == 0) p.lse[row] = -INFINITY;
-    return;
-  }
-  const long long u0 = warp_sum(before) * per_b + static_cast<long long>(h * p.row_blocks + rb) * T;
-  const int c0 = runs.cta_of(u0), c1 = runs.cta_of(u0 + T - 1);
-  if (c0 == c1) return;
-  // part of CTA c: its first segment, except where it came to this item from another
-  auto slot_of = [&](int c) { return 2 * c + (c == c0 && runs.start(c0) < u0 ? 1 : 0); };
-  float M = -INFINITY, L = 0.f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0 + warp; c <= c1; c += 4) {
-    const size_t at = static_cast<size_t>(slot_of(c)) * ROWS + r;
-    const float2 x = __ldcg(p.part_ml + at);
-    const float4 v = lane < V4 ? __ldcg(reinterpret_cast<const float4*>(p.part_o) + at * V4 + lane) : a;
-    const float Mn = fmaxf(M, x.x);
-    const float Mu = Mn == -INFINITY ? 0.f : Mn;
-    const float fo = b200::ex2_approx(M - Mu), fn = b200::ex2_approx(x.x - Mu);
-    L = L * fo + x.y * fn;
-    a.x = a.x * fo + v.x * fn, a.y = a.y * fo + v.y * fn, a.z = a.z * fo + v.z * fn, a.w = a.w * fo + v.w * fn;
+  const Kv4Head hd = p.heads[blockIdx.x];
+  if (hd.parts == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int R = p.Hq / p.c.H * p.N, n = kv4_qlen(p, hd.b);
+  const int r = blockIdx.y * 8 + warp, rr = hd.rb * ROWS + r;
+  if (rr >= R || rr % p.N >= n) return;
+  float M = -INFINITY, L = 0.f, a[E] = {};
+  for (int i0 = 0; i0 < hd.parts; i0 += 32) {
+    auto at = [&](int i) {
+      return static_cast<size_t>(i == 0 ? hd.slot : 2 * (static_cast<int>(blockIdx.x) + i)) * ROWS + r;
+    };
+    const int i = i0 + lane;
+    const float2 x = i < hd.parts ? __ldcg(p.part_ml + at(i)) : make_float2(-INFINITY, 0.f);
+    float mx = x.x;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+    const float Mn = fmaxf(M, mx), Mu = Mn == -INFINITY ? 0.f : Mn;
+    const float fo = b200::ex2_approx(M - Mu), mine = b200::ex2_approx(x.x - Mu);
+    // (a part whose keys lie behind this row's has no O: nothing was written)
+    const uint32_t full = __ballot_sync(0xffffffffu, !(x.x == -INFINITY && x.y == 0.f));
+    float sum = x.y * mine;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    L = L * fo + sum;
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] *= fo;
+    const int m = min(32, hd.parts - i0);
+#pragma unroll 8
+    for (int k = 0; k < m; ++k) {
+      const float f = __shfl_sync(0xffffffffu, mine, k);
+      const bool have = (full >> k) & 1u;
+      const float* src = p.part_o + at(i0 + k) * D + lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[e] += f * (have ? __ldcg(src + 32 * e) : 0.f);
+    }
     M = Mn;
   }
-  if (lane < V4) so[warp][lane] = a;
-  if (lane == 0) sml[warp] = make_float2(M, L);
-  __syncthreads();
-  if (tid >= V4) return;
-  M = fmaxf(fmaxf(sml[0].x, sml[1].x), fmaxf(sml[2].x, sml[3].x));
-  const float Mu = M == -INFINITY ? 0.f : M;
-  L = 0.f;
-  a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = b200::ex2_approx(sml[w].x - Mu);
-    const float4 v = so[w][tid];
-    L += f * sml[w].y;
-    a.x += f * v.x, a.y += f * v.y, a.z += f * v.z, a.w += f * v.w;
-  }
   const float inv = L == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / L;
-  reinterpret_cast<uint2*>(p.o)[row * V4 + tid] =
-      make_uint2(pack_16<F16>(a.x * inv, a.y * inv), pack_16<F16>(a.z * inv, a.w * inv));
-  if (p.lse != nullptr && tid == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+  const size_t row = (static_cast<size_t>(hd.b) * p.c.H + hd.h) * R + rr;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    reinterpret_cast<uint16_t*>(p.o)[row * D + lane + 32 * e] = static_cast<uint16_t>(pack_16<F16>(a[e] * inv, 0.f));
+  if (p.lse != nullptr && lane == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
 }
 
 }  // namespace attn

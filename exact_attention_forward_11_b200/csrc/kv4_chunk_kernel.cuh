@@ -15,7 +15,7 @@
 //  * The 128-key tiles of all units make one list that is cut into equal runs, one per CTA, as in
 //    kv4_attn_kernel.cuh (causal units count only the tiles that their rows see): 148 CTAs of
 //    equal work whatever the lengths. A unit that several runs share is joined by
-//    kv4_chunk_join_sm100 from fp32 parts in the workspace, in the order of the runs.
+//    kv4_join_sm100 from fp32 parts in the workspace, in the order of the runs.
 //
 //  * With at most 128 rows (PAIR) a unit has one row tile, which would leave one softmax group idle and
 //    make every step a chain; there both groups work on the same rows, group t on every second key
@@ -86,15 +86,8 @@ constexpr int kNoTile = static_cast<int>(0x80000000u);
 template <int D>
 struct SfWords { static constexpr int N = D / 64; };   // 32-bit words of a row's scale bytes
 
-// A unit's first part, as the CTA that wrote it leaves it for the join.
-struct Kv4Head {
-  int parts;                 // 0: this CTA has none
-  int b, h, qp, slot;
-};
-
 struct Kv4ChunkParams {
   Kv4AttnParams a;           // part_o: [2 ctas][256][D], part_ml: [2 ctas][256]; row_blocks = ceil(R / 256)
-  Kv4Head* heads;            // [ctas]
   uint64_t timeout_cycles;
 };
 
@@ -188,23 +181,6 @@ struct Kv4ChunkWalk {
   }
   __device__ __forceinline__ bool whole() const { return kt0 == 0 && kt1 == nkv; }
 };
-
-// O = 0, LSE = -infinity for the rows that see no key.
-template <int D>
-__device__ __forceinline__ void kv4_empty_rows(const Kv4AttnParams& p, int thread, int threads) {
-  for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
-    const int len = kv4_len(p.c, b), n = kv4_qlen(p, b);
-    const int z = len == 0 ? n : (p.causal ? max(0, n - len) : 0);
-    if (z == 0) continue;
-    constexpr int V4 = D / 8;                        // 16-byte pieces of a row
-    for (long long i = thread; i < static_cast<long long>(p.Hq) * z * V4; i += threads) {
-      const long long r = i / V4;
-      const size_t row = (static_cast<size_t>(b) * p.Hq + r / z) * p.N + r % z;
-      reinterpret_cast<uint4*>(p.o)[row * V4 + i % V4] = make_uint4(0u, 0u, 0u, 0u);
-      if (p.lse != nullptr && i % V4 == 0) p.lse[row] = -INFINITY;
-    }
-  }
-}
 
 template <class C, bool F16>
 __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkParams cp) {
@@ -415,7 +391,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
       if (!idle) w.seek(u0, u1, lane);
       w.u = u0;
       w.u_end = u1;
-      if (lane == 0) cp.heads[blockIdx.x].parts = 0;
+      if (lane == 0) p.heads[blockIdx.x].parts = 0;
       const uint32_t slot_mask = (1u << p.c.page_shift) - 1u;
       uint32_t k = 0;
       for (uint32_t sg = 0; ok; ++sg) {
@@ -434,8 +410,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
           if (!over && w.kt0 == 0 && !w.whole()) {    // the unit's first part: what the join needs
             Kv4Head hd;
             hd.parts = runs.cta_of(w.u - w.kt1 + w.nkv - 1) - static_cast<int>(blockIdx.x) + 1;
-            hd.b = w.b, hd.h = w.h, hd.qp = w.qp, hd.slot = x.slot;
-            cp.heads[blockIdx.x] = hd;
+            hd.b = w.b, hd.h = w.h, hd.rb = w.qp, hd.slot = x.slot;
+            p.heads[blockIdx.x] = hd;
           }
           mbar_arrive(seg_full + sg % C::RING);
         }
@@ -835,59 +811,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
   __syncthreads();
   tc_fence_after();
   if (warp == C::MMA_WARP) tmem_dealloc(tmem_base, C::TMEM_COLS);
-}
-
-// Joins the parts of the unit whose first part CTA blockIdx.x wrote: a warp per row. A lane holds the
-// (maximum, sum) of one part, so that the parts' O, D / 32 channels a lane, load without waiting for
-// one another.
-template <class C, bool F16>
-__global__ void __launch_bounds__(256) kv4_chunk_join_sm100(const Kv4ChunkParams cp) {
-  constexpr int D = C::D, E = D / 32;
-  const Kv4AttnParams& p = cp.a;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Kv4Head hd = cp.heads[blockIdx.x];
-  if (hd.parts == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int R = p.Hq / p.c.H * p.N, n = kv4_qlen(p, hd.b);
-  const int r = blockIdx.y * 8 + warp, rr = hd.qp * kChunkRows + r;
-  if (rr >= R || rr % p.N >= n) return;
-  float M = -INFINITY, L = 0.f, a[E] = {};
-  for (int i0 = 0; i0 < hd.parts; i0 += 32) {
-    auto at = [&](int i) {
-      return static_cast<size_t>(i == 0 ? hd.slot : 2 * (static_cast<int>(blockIdx.x) + i)) * kChunkRows + r;
-    };
-    const int i = i0 + lane;
-    const float2 x = i < hd.parts ? __ldcg(p.part_ml + at(i)) : make_float2(-INFINITY, 0.f);
-    float mx = x.x;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-    const float Mn = fmaxf(M, mx), Mu = Mn == -INFINITY ? 0.f : Mn;
-    const float fo = b200::ex2_approx(M - Mu), mine = b200::ex2_approx(x.x - Mu);
-    // (a part whose keys lie behind this row's has no O: nothing was written)
-    const uint32_t full = __ballot_sync(0xffffffffu, !(x.x == -INFINITY && x.y == 0.f));
-    float sum = x.y * mine;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-    L = L * fo + sum;
-#pragma unroll
-    for (int e = 0; e < E; ++e) a[e] *= fo;
-    const int m = min(32, hd.parts - i0);
-#pragma unroll 8
-    for (int k = 0; k < m; ++k) {
-      const float f = __shfl_sync(0xffffffffu, mine, k);
-      const bool have = (full >> k) & 1u;
-      const float* src = p.part_o + at(i0 + k) * D + lane;
-#pragma unroll
-      for (int e = 0; e < E; ++e) a[e] += f * (have ? __ldcg(src + 32 * e) : 0.f);
-    }
-    M = Mn;
-  }
-  const float inv = L == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / L;
-  const size_t row = (static_cast<size_t>(hd.b) * p.c.H + hd.h) * R + rr;
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    reinterpret_cast<uint16_t*>(p.o)[row * D + lane + 32 * e] = static_cast<uint16_t>(pack_16<F16>(a[e] * inv, 0.f));
-  if (p.lse != nullptr && lane == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
 }
 
 }  // namespace attn

@@ -93,7 +93,7 @@ ATTN_API attn_status attn_kv4_read(const void* k_codes, const void* k_sf, const 
  *          NaN; rows that do not see it are unaffected.
  *   workspace : at least attn_fwd_kv4_workspace_bytes(...) bytes, 16-byte aligned,
  *          overwritten; needs no initialisation. Calls that overlap on the GPU need
- *          separate workspaces. May be NULL if that size is 0.
+ *          separate workspaces.
  *   scale: 0 selects 1/sqrt(d).
  * Arithmetic: scores and P V on f16 tensor-core products with fp32 accumulation
  * (every cached value is exact in f16; a query row is scaled by a power of two to

@@ -450,3 +450,44 @@ def test_decoding_run(cuda_lib):
             bt = pg.bt[b].cpu().numpy()
             assert (kv4_rows(codes.cpu().numpy(), bt, page, 0, lens[b]) == c).all()
             assert (kv4_rows(sf.cpu().numpy(), bt, page, 0, lens[b]) == s).all()
+
+
+def test_one_workspace_for_calls_of_every_shape(cuda_lib):
+    """A caller's workspace, full of anything, used by calls of different shapes in turn: the results
+    are those of the binding's own, and nothing behind the required size is written."""
+    lib, d = cuda_lib, 128
+    pg = Paged(lib, 3, 2, d, 16, 200, seed=8)
+    lens = [3100, 900, 17]
+    fill(pg, lens, torch.bfloat16, 6)
+    small = Paged(lib, 1, 1, 64, 32, 40, seed=9)
+    fill(small, [1200], torch.bfloat16, 7)
+    jobs = [(pg, lens, 1, 4), (small, [1200], 1, 2), (pg, lens, 150, 2), (pg, lens, 5, 4), (small, [1200], 40, 2),
+            (pg, lens, 40, 4), (small, [1200], 3, 5), (pg, lens, 1, 4)]
+    need = [lib.attn_fwd_kv4_workspace_bytes(g.B, hq, g.H, N, g.d, g.page, g.max_pages) for g, _, N, hq in jobs]
+    ws = torch.full((max(need) + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+    for (g, ln, N, hq), nb in zip(jobs, need):
+        q = make_q(g.B, hq, N, g.d, torch.bfloat16, N)
+        want = lib.forward_kv4(q, g.cache, g.bt, ints(ln), causal=True, check=True)
+        ws[nb:] = 0x5A
+        o, lse = lib.forward_kv4(q, g.cache, g.bt, ints(ln), causal=True, workspace=ws, check=True)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        assert (ws[nb:] == 0x5A).all()
+    with pytest.raises(ValueError):
+        lib.forward_kv4(q, g.cache, g.bt, ints(ln), workspace=ws[:need[-1] - 1])
+
+
+@pytest.mark.parametrize("N", [1, 3])
+def test_many_sequences(cuda_lib, N):
+    """More sequences than a warp has lanes, most of them short, some empty, one long."""
+    lib, B, d = cuda_lib, 77, 64
+    lens = [(7 * b * b + 3 * b) % 90 for b in range(B)]
+    lens[50], lens[3], lens[76] = 1500, 0, 0
+    pg = Paged(lib, B, 2, d, 16, 94, seed=N)
+    fill(pg, lens, torch.float16, 5)
+    q = make_q(B, 6, N, d, torch.float16, 3)
+    o, lse = lib.forward_kv4(q, pg.cache, pg.bt, ints(lens), causal=True, check=True)
+    check_attention(o, lse, q, pg, lens, [N] * B, True)
+    big = make_q(B, 2, 150, d, torch.float16, 4)                 # chunks of all of them
+    o, lse = lib.forward_kv4(big, pg.cache, pg.bt, ints(lens), q_lens=ints([min(150, x) for x in lens]), causal=True,
+                             check=True)
+    check_attention(o, lse, big, pg, lens, [min(150, x) for x in lens], True, rows=(0, 1, 40, 149))
