@@ -673,7 +673,7 @@ def kv4_append(cache, k, v, block_table, seq_lens, new_lens=None, stream=None, c
     nl = None if new_lens is None else _kv4_int32(new_lens, "new_lens", (B,), cache.device)
     sp, place = _kv4_stream(cache, stream)
     try:
-        _check(attn_kv4_append(k.data_ptr(), v.data_ptr(), *cache._ptrs, bt, sl, nl, B, H, N, cache.d,
+        _check(load().attn_kv4_append(k.data_ptr(), v.data_ptr(), *cache._ptrs, bt, sl, nl, B, H, N, cache.d,
                                cache.num_pages, cache.page_size, max_pages, cache.k_exp, cache.v_exp, dt, sp),
                "attn_kv4_append")
         if check:
@@ -703,7 +703,7 @@ def kv4_read(cache, block_table, seq_lens, N, starts=None, dtype=None, k=None, v
         if v is None:
             v = torch.empty_like(k)
         _kv4_like(v, "v", k)
-        _check(attn_kv4_read(*cache._ptrs, bt, sl, st, k.data_ptr(), v.data_ptr(), B, H, N, cache.d, cache.num_pages,
+        _check(load().attn_kv4_read(*cache._ptrs, bt, sl, st, k.data_ptr(), v.data_ptr(), B, H, N, cache.d, cache.num_pages,
                              cache.page_size, max_pages, cache.k_exp, cache.v_exp, dt, sp), "attn_kv4_read")
         if check:
             _check_device(check, sp, "attn_kv4_read")
@@ -769,7 +769,7 @@ def forward_kv4(q, cache, block_table, seq_lens, q_lens=None, causal=False, scal
         elif workspace.device != q.device or workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or \
                 workspace.numel() < need:
             raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {q.device}")
-        _check(attn_fwd_kv4(q.data_ptr(), *cache._ptrs, bt, sl, ql, out.data_ptr(),
+        _check(load().attn_fwd_kv4(q.data_ptr(), *cache._ptrs, bt, sl, ql, out.data_ptr(),
                             None if lse is None else lse.data_ptr(),
                             None if workspace is None else workspace.data_ptr(),
                             0 if workspace is None else workspace.numel(), B, Hq, cache.heads, N, cache.d,

@@ -47,15 +47,6 @@ attn::Kv4Cache kv4_cache_of(const void* k_codes, const void* k_sf, const void* v
   return c;
 }
 
-// Grid of the two moving kernels: a thread per 16-value block of K (y = 0) and V
-// (y = 1), at most 16 CTAs of 256 threads per SM in all (a grid-stride loop covers
-// the rest).
-dim3 kv4_move_grid(long long blocks, int sms) {
-  const long long need = (blocks + attn::kKv4Threads - 1) / attn::kKv4Threads;
-  const long long cap = 8ll * sms;
-  return dim3(static_cast<unsigned>(need < cap ? need : cap), 2);
-}
-
 // How attn_fwd_kv4 runs a shape (host only; it assumes the SMs of a B200, so that the
 // workspace's size does not depend on the current device): by the query rows of one cached head.
 struct Kv4Plan {
@@ -153,8 +144,6 @@ attn_status attn_kv4_append(const void* k, const void* v, void* k_codes, void* k
       s != ATTN_OK)
     return s;
   if (!aligned16(k) || !aligned16(v) || !aligned4(new_lens)) return ATTN_ERR_MISALIGNED;
-  const int sms = sm_count();
-  if (sms <= 0) return ATTN_ERR_CUDA;
   attn::Kv4MoveParams p{};
   p.c = kv4_cache_of(k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, B, Hkv, num_pages, page_size, max_pages,
                      k_exp, v_exp);
@@ -162,10 +151,10 @@ attn_status attn_kv4_append(const void* k, const void* v, void* k_codes, void* k
   p.in[1] = static_cast<const uint8_t*>(v);
   p.first = new_lens;
   p.N = N;
-  p.blocks = static_cast<long long>(B) * Hkv * N * (d / 16);
+  p.tiles = (N + attn::kKv4Rows - 1) / attn::kKv4Rows;
   auto kern = d == 128 ? (dtype == ATTN_FP16 ? attn::kv4_append_sm100<128, true> : attn::kv4_append_sm100<128, false>)
                        : (dtype == ATTN_FP16 ? attn::kv4_append_sm100<64, true> : attn::kv4_append_sm100<64, false>);
-  kern<<<kv4_move_grid(p.blocks, sms), attn::kKv4Threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  kern<<<dim3(static_cast<unsigned>(B * Hkv * p.tiles), 2), attn::kKv4Threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -179,8 +168,6 @@ attn_status attn_kv4_read(const void* k_codes, const void* k_sf, const void* v_c
       s != ATTN_OK)
     return s;
   if (!aligned16(k) || !aligned16(v) || !aligned4(starts)) return ATTN_ERR_MISALIGNED;
-  const int sms = sm_count();
-  if (sms <= 0) return ATTN_ERR_CUDA;
   attn::Kv4MoveParams p{};
   p.c = kv4_cache_of(k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, B, Hkv, num_pages, page_size, max_pages,
                      k_exp, v_exp);
@@ -188,10 +175,10 @@ attn_status attn_kv4_read(const void* k_codes, const void* k_sf, const void* v_c
   p.out[1] = static_cast<uint8_t*>(v);
   p.first = starts;
   p.N = N;
-  p.blocks = static_cast<long long>(B) * Hkv * N * (d / 16);
+  p.tiles = (N + attn::kKv4Rows - 1) / attn::kKv4Rows;
   auto kern = d == 128 ? (dtype == ATTN_FP16 ? attn::kv4_read_sm100<128, true> : attn::kv4_read_sm100<128, false>)
                        : (dtype == ATTN_FP16 ? attn::kv4_read_sm100<64, true> : attn::kv4_read_sm100<64, false>);
-  kern<<<kv4_move_grid(p.blocks, sms), attn::kKv4Threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  kern<<<dim3(static_cast<unsigned>(B * Hkv * p.tiles), 2), attn::kKv4Threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -215,17 +215,17 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
   const bool few = p.c.B <= 32;
   int my_len = 0, my_n = 0;                         // of sequence `lane`, if few
   long long total = 0;
+  bool blind = false;                               // some row sees no key
   for (int i = lane; i < p.c.B; i += 32) {
     my_len = kv4_len(p.c, i);
     my_n = kv4_qlen(p, i);
     total += my_n == 0 ? 0 : (my_len + kDecTile - 1) / kDecTile;
+    blind = blind || (my_n > 0 && (my_len == 0 || (p.causal && my_n > my_len)));
   }
+  if (__any_sync(0xffffffffu, blind)) kv4_empty_rows<D>(p, tid, kDecWarps * 32);
   const long long my_units = total * per_b;
   const Kv4Runs runs(warp_sum(my_units), p.ctas);
-  if (static_cast<int>(blockIdx.x) >= runs.n) {
-    kv4_empty_rows<D>(p, tid, kDecWarps * 32);
-    return;
-  }
+  if (static_cast<int>(blockIdx.x) >= runs.n) return;
   long long u = runs.start(blockIdx.x);
   const long long u_begin = u, u_end = runs.start(blockIdx.x + 1);
   int b = 0;
@@ -655,11 +655,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
         if (d4 == 0) p.part_ml[static_cast<size_t>(slot) * ROWS + r] = make_float2(M, L);
       }
     }
-    if (!more) break;
+    if (!more) return;
     __syncthreads();
     if constexpr (NT > 1) issue_next(NT - 1);
   }
-  kv4_empty_rows<D>(p, tid, kDecWarps * 32);
 }
 
 // Joins the parts of the item whose first part CTA blockIdx.x wrote (row blocks of ROWS rows): a warp per

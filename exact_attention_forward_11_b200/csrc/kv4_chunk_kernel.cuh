@@ -81,7 +81,6 @@ struct __align__(16) Kv4Seg {
   unsigned long long row;    // row of (b, h, 0) in q and o
 };
 static_assert(sizeof(Kv4Seg) <= 64, "segment ring");
-constexpr uint32_t kNoRow = 0xFFFFFFFFu;       // a key behind the end
 constexpr int kNoTile = static_cast<int>(0x80000000u);
 template <int D>
 struct SfWords { static constexpr int N = D / 64; };   // 32-bit words of a row's scale bytes
@@ -325,55 +324,55 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
             if (j + 2 < nt && !(ok = s_of(t, k + 2))) break;
           }
           if (!ok) break;
-          continue;
-        }
-        // S of the segment's first tile (issued after the previous segment's last P V on this
-        // thread, so it overwrites that P only after it has been read)
+        } else {
+          // S of the segment's first tile (issued after the previous segment's last P V on this
+          // thread, so it overwrites that P only after it has been read)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (w.end[t] > w.kt0) {
-            if (!(ok = wait_all(q_full + t, (qc >> t) & 1u))) break;
-            qc ^= 1u << t;
-          }
-        if (!ok || !(ok = wait_all(k_full + (k & 1), (k >> 1) & 1))) break;
-        tc_fence_after();
+          for (int t = 0; t < 2; ++t)
+            if (w.end[t] > w.kt0) {
+              if (!(ok = wait_all(q_full + t, (qc >> t) & 1u))) break;
+              qc ^= 1u << t;
+            }
+          if (!ok || !(ok = wait_all(k_full + (k & 1), (k >> 1) & 1))) break;
+          tc_fence_after();
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (w.end[t] > w.kt0) {
-            issue_s(t, k & 1);
-            commit(s_full + t);
-          }
-        commit(k_empty + (k & 1));
-        for (int j = w.kt0; j < w.kt1; ++j, ++k) {
-          const uint32_t k1 = k + 1;
-          if (!(ok = wait_all(v_full + (k & 1), (k >> 1) & 1))) break;
-          bool k_ready = false;
+          for (int t = 0; t < 2; ++t)
+            if (w.end[t] > w.kt0) {
+              issue_s(t, k & 1);
+              commit(s_full + t);
+            }
+          commit(k_empty + (k & 1));
+          for (int j = w.kt0; j < w.kt1; ++j, ++k) {
+            const uint32_t k1 = k + 1;
+            if (!(ok = wait_all(v_full + (k & 1), (k >> 1) & 1))) break;
+            bool k_ready = false;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (j >= w.end[t]) continue;
+            for (int t = 0; t < 2; ++t) {
+              if (j >= w.end[t]) continue;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (!(ok = wait_all(p_full + 2 * t + c, (pc >> t) & 1u))) break;
-              tc_fence_after();
-              issue_pv(t, k & 1, c, j > w.kt0 || c > 0);
+              for (int c = 0; c < 2; ++c) {
+                if (!(ok = wait_all(p_full + 2 * t + c, (pc >> t) & 1u))) break;
+                tc_fence_after();
+                issue_pv(t, k & 1, c, j > w.kt0 || c > 0);
+              }
+              if (!ok) break;
+              pc ^= 1u << t;
+              if (j + 1 < w.end[t]) {
+                if (!k_ready) {
+                  if (!(ok = wait_all(k_full + (k1 & 1), (k1 >> 1) & 1))) break;
+                  k_ready = true;
+                  tc_fence_after();
+                }
+                issue_s(t, k1 & 1);
+                commit(s_full + t);
+              } else {
+                commit(o_done + t);
+              }
             }
             if (!ok) break;
-            pc ^= 1u << t;
-            if (j + 1 < w.end[t]) {
-              if (!k_ready) {
-                if (!(ok = wait_all(k_full + (k1 & 1), (k1 >> 1) & 1))) break;
-                k_ready = true;
-                tc_fence_after();
-              }
-              issue_s(t, k1 & 1);
-              commit(s_full + t);
-            } else {
-              commit(o_done + t);
-            }
+            commit(v_empty + (k & 1));
+            if (k_ready) commit(k_empty + (k1 & 1));
           }
-          if (!ok) break;
-          commit(v_empty + (k & 1));
-          if (k_ready) commit(k_empty + (k1 & 1));
         }
         if (!ok) break;
       }
@@ -554,7 +553,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
     // ======================= softmax: one thread per row =======================
     regs_increase<C::REGS_SOFTMAX>();
     const int t = warp >> 2, wq = warp & 3;
-    const int r = wq * 32 + lane;                     // row inside the tile
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t s_tm = tmem_base + lane_off + t * 128;
     const uint32_t o_tm = tmem_base + lane_off + C::O_COL0 + t * D;
