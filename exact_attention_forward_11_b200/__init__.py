@@ -49,9 +49,9 @@ SIGNATURES = {
     "attn_fwd_debug_row_limit": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, ctypes.c_longlong, _P]),
     "attn_debug_build": (_I, []),
     "attn_debug_last_failure": (_I, [ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_longlong), _P]),
-    "attn_kv4_append": (_I, [_P] * 9 + [_I] * 10 + [_P]),
-    "attn_kv4_read": (_I, [_P] * 9 + [_I] * 10 + [_P]),
-    "attn_fwd_kv4": (_I, [_P] * 11 + [ctypes.c_size_t] + [_I] * 10 + [_F, _I, _I, _P]),
+    "attn_kv4_append": (_I, [_P] * 6 + [_I] * 4 + [_P]),
+    "attn_kv4_read": (_I, [_P] * 6 + [_I] * 4 + [_P]),
+    "attn_fwd_kv4": (_I, [_P] * 8 + [ctypes.c_size_t] + [_I] * 4 + [_F, _I, _I, _P]),
     "attn_fwd_kv4_workspace_bytes": (ctypes.c_size_t, [_I] * 7),
     "attn_status_string": (ctypes.c_char_p, [_I]),
     "attn_abi_version": (_I, []),
@@ -170,23 +170,24 @@ def attn_debug_last_failure(stream):
     return site.value, index.value
 
 
-def attn_kv4_append(k, v, k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, new_lens, B, Hkv, N, d, num_pages,
-                    page_size, max_pages, k_exp, v_exp, dtype, stream):
-    return load().attn_kv4_append(k, v, k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, new_lens, B, Hkv, N, d,
-                                  num_pages, page_size, max_pages, k_exp, v_exp, dtype, stream)
+class attn_kv4_cache(ctypes.Structure):
+    """The cache struct of include/kv4_b200.h; the calls take its address (ctypes.addressof)."""
+    _fields_ = [(n, _P) for n in ("k_codes", "k_sf", "v_codes", "v_sf")] + \
+               [(n, _I) for n in ("num_pages", "page_size", "Hkv", "d", "k_exp", "v_exp")]
 
 
-def attn_kv4_read(k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, starts, k, v, B, Hkv, N, d, num_pages,
-                  page_size, max_pages, k_exp, v_exp, dtype, stream):
-    return load().attn_kv4_read(k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, starts, k, v, B, Hkv, N, d,
-                                num_pages, page_size, max_pages, k_exp, v_exp, dtype, stream)
+def attn_kv4_append(cache, k, v, block_table, seq_lens, new_lens, B, N, max_pages, dtype, stream):
+    return load().attn_kv4_append(cache, k, v, block_table, seq_lens, new_lens, B, N, max_pages, dtype, stream)
 
 
-def attn_fwd_kv4(q, k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, q_lens, o, lse, workspace, workspace_bytes,
-                 B, Hq, Hkv, N, d, num_pages, page_size, max_pages, k_exp, v_exp, scale, causal, dtype, stream):
-    return load().attn_fwd_kv4(q, k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, q_lens, o, lse, workspace,
-                               workspace_bytes, B, Hq, Hkv, N, d, num_pages, page_size, max_pages, k_exp, v_exp,
-                               scale, causal, dtype, stream)
+def attn_kv4_read(cache, block_table, seq_lens, starts, k, v, B, N, max_pages, dtype, stream):
+    return load().attn_kv4_read(cache, block_table, seq_lens, starts, k, v, B, N, max_pages, dtype, stream)
+
+
+def attn_fwd_kv4(cache, q, block_table, seq_lens, q_lens, o, lse, workspace, workspace_bytes, B, Hq, N, max_pages,
+                 scale, causal, dtype, stream):
+    return load().attn_fwd_kv4(cache, q, block_table, seq_lens, q_lens, o, lse, workspace, workspace_bytes, B, Hq, N,
+                               max_pages, scale, causal, dtype, stream)
 
 
 def attn_fwd_kv4_workspace_bytes(B, Hq, Hkv, N, d, page_size, max_pages):
@@ -566,9 +567,10 @@ class KV4Cache:
     above 2000."""
 
     __slots__ = ("k_codes", "k_sf", "v_codes", "v_sf", "k_exp", "v_exp", "num_pages", "heads", "page_size", "d",
-                 "device", "_ptrs", "_need")
+                 "device", "_index", "_struct", "_addr", "_need")
 
     def __init__(self, k_codes, k_sf, v_codes, v_sf, k_exp=0, v_exp=0):
+        global torch     # the cache calls below run at the rate of decoding steps: no import in each
         import torch
         if k_codes.dim() != 4:
             raise ValueError("k_codes must be [num_pages, Hkv, page_size, d / 2]")
@@ -581,7 +583,10 @@ class KV4Cache:
         self.k_codes, self.k_sf, self.v_codes, self.v_sf = k_codes, k_sf, v_codes, v_sf
         self.k_exp, self.v_exp = int(k_exp), int(v_exp)
         self.num_pages, self.heads, self.page_size, self.d, self.device = P, H, S, 2 * half, k_codes.device
-        self._ptrs = tuple(t.data_ptr() for t in (k_codes, k_sf, v_codes, v_sf))
+        self._index = k_codes.get_device()
+        self._struct = attn_kv4_cache(*(t.data_ptr() for t in (k_codes, k_sf, v_codes, v_sf)), P, S, H, 2 * half,
+                                      self.k_exp, self.v_exp)
+        self._addr = ctypes.addressof(self._struct)
         self._need = {}      # workspace bytes of forward_kv4 by (B, Hq, N, max_pages)
 
     @classmethod
@@ -593,39 +598,37 @@ class KV4Cache:
         return cls(*new, k_exp=k_exp, v_exp=v_exp)
 
 
-def _kv4_int32(t, name, size, device):
-    import torch
-    if t.dtype is not torch.int32 or t.shape != size or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(size)} on {device}")
+def _kv4_int32(t, name, shape, cache):
+    if t.dtype is not torch.int32 or t.get_device() != cache._index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {cache.device}")
     return t.data_ptr()
 
 
-def _kv4_rows(t, name, cache, heads=None):
+def _kv4_rows(t, name, cache):
     """Sizes and element type of a 16-bit [B, H, N, d] argument of the cache calls."""
-    import torch
     dt = t.dtype
     shape = t.shape
-    if len(shape) != 4 or t.device != cache.device or not t.is_contiguous() or \
+    if len(shape) != 4 or t.get_device() != cache._index or not t.is_contiguous() or \
             (dt is not torch.bfloat16 and dt is not torch.float16):
         raise ValueError(f"{name} must be a contiguous bf16 or fp16 tensor [B, H, N, d] on {cache.device}")
     B, H, N, d = shape
-    if d != cache.d or (heads is not None and H != heads):
-        raise ValueError(f"{name} has {H} heads of width {d}: the cache has {cache.heads} of {cache.d}")
+    if d != cache.d:
+        raise ValueError(f"{name} has heads of width {d}: the cache has {cache.d}")
     return B, H, N, ATTN_BF16 if dt is torch.bfloat16 else ATTN_FP16
 
 
 def _kv4_like(t, name, ref):
     """A tensor argument that must be like `ref`."""
-    if t.shape != ref.shape or t.dtype is not ref.dtype or t.device != ref.device or not t.is_contiguous():
+    if t.shape != ref.shape or t.dtype is not ref.dtype or t.get_device() != ref.get_device() or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {ref.dtype} tensor of shape {tuple(ref.shape)} on {ref.device}")
+    return t.data_ptr()
 
 
-def _kv4_tables(cache, block_table, seq_lens, B):
-    shape = block_table.shape
+def _kv4_table(t, B, cache):
+    shape = t.shape
     if len(shape) != 2 or shape[0] != B:
         raise ValueError(f"block_table must be int32 [{B}, max_pages]")
-    return _kv4_int32(block_table, "block_table", shape, cache.device), \
-        _kv4_int32(seq_lens, "seq_lens", (B,), cache.device), shape[1]
+    return _kv4_int32(t, "block_table", shape, cache), shape[1]
 
 
 class _kv4_place:
@@ -635,7 +638,6 @@ class _kv4_place:
     __slots__ = ("ctx", "sp")
 
     def __init__(self, device, stream):
-        import torch
         self.ctx = [torch.cuda.device(device)]
         if stream is not None:
             self.ctx.append(torch.cuda.stream(stream))
@@ -651,8 +653,7 @@ class _kv4_place:
 def _kv4_stream(cache, stream):
     """(raw stream, place to leave or None): nothing to switch in the usual case, the
     current stream of the current device."""
-    import torch
-    index = cache.device.index
+    index = cache._index
     if stream is None and index == torch._C._cuda_getDevice():
         return torch._C._cuda_getCurrentRawStream(index), None
     place = _kv4_place(cache.device, stream)
@@ -667,16 +668,17 @@ def kv4_append(cache, k, v, block_table, seq_lens, new_lens=None, stream=None, c
     block_table[b, position // page_size]. Asynchronous; a page number or length outside
     the cache skips the write and is reported by attn_get_device_status()
     (check=True waits and raises). Returns the cache."""
-    B, H, N, dt = _kv4_rows(k, "k", cache, cache.heads)
-    _kv4_like(v, "v", k)
-    bt, sl, max_pages = _kv4_tables(cache, block_table, seq_lens, B)
-    nl = None if new_lens is None else _kv4_int32(new_lens, "new_lens", (B,), cache.device)
+    B, H, N, dt = _kv4_rows(k, "k", cache)
+    if H != cache.heads:
+        raise ValueError(f"k has {H} heads: the cache has {cache.heads}")
+    bt, max_pages = _kv4_table(block_table, B, cache)
+    args = (cache._addr, k.data_ptr(), _kv4_like(v, "v", k), bt, _kv4_int32(seq_lens, "seq_lens", (B,), cache),
+            None if new_lens is None else _kv4_int32(new_lens, "new_lens", (B,), cache), B, N, max_pages, dt)
     sp, place = _kv4_stream(cache, stream)
     try:
-        _check(load().attn_kv4_append(k.data_ptr(), v.data_ptr(), *cache._ptrs, bt, sl, nl, B, H, N, cache.d,
-                               cache.num_pages, cache.page_size, max_pages, cache.k_exp, cache.v_exp, dt, sp),
-               "attn_kv4_append")
-        if check:
+        st = load().attn_kv4_append(*args, sp)
+        if st or check:
+            _check(st, "attn_kv4_append")
             _check_device(check, sp, "attn_kv4_append")
     finally:
         if place is not None:
@@ -688,24 +690,23 @@ def kv4_read(cache, block_table, seq_lens, N, starts=None, dtype=None, k=None, v
     """K, V (bf16 or fp16 [B, Hkv, N, d]) read back from the cache: row i holds position
     starts[b] + i (None: i); rows at or behind seq_lens[b] are zero. Asynchronous;
     bad page numbers and lengths as in kv4_append."""
-    import torch
     B = seq_lens.shape[0]
-    bt, sl, max_pages = _kv4_tables(cache, block_table, seq_lens, B)
-    st = None if starts is None else _kv4_int32(starts, "starts", (B,), cache.device)
+    bt, max_pages = _kv4_table(block_table, B, cache)
+    sl = _kv4_int32(seq_lens, "seq_lens", (B,), cache)
+    first = None if starts is None else _kv4_int32(starts, "starts", (B,), cache)
     sp, place = _kv4_stream(cache, stream)
     try:
         if k is None:
             k = torch.empty((B, cache.heads, N, cache.d), dtype=torch.bfloat16 if dtype is None else dtype,
                             device=cache.device)
-        kB, H, kN, dt = _kv4_rows(k, "k", cache, cache.heads)
-        if kB != B or kN != N or (dtype is not None and k.dtype is not dtype):
-            raise ValueError(f"k must be [{B}, {H}, {N}, {cache.d}]" + ("" if dtype is None else f" of {dtype}"))
+        kB, H, kN, dt = _kv4_rows(k, "k", cache)
+        if kB != B or kN != N or H != cache.heads or (dtype is not None and k.dtype is not dtype):
+            raise ValueError(f"k must be [{B}, {cache.heads}, {N}, {cache.d}]" + ("" if dtype is None else f" of {dtype}"))
         if v is None:
             v = torch.empty_like(k)
-        _kv4_like(v, "v", k)
-        _check(load().attn_kv4_read(*cache._ptrs, bt, sl, st, k.data_ptr(), v.data_ptr(), B, H, N, cache.d, cache.num_pages,
-                             cache.page_size, max_pages, cache.k_exp, cache.v_exp, dt, sp), "attn_kv4_read")
-        if check:
+        st = load().attn_kv4_read(cache._addr, bt, sl, first, k.data_ptr(), _kv4_like(v, "v", k), B, N, max_pages, dt, sp)
+        if st or check:
+            _check(st, "attn_kv4_read")
             _check_device(check, sp, "attn_kv4_read")
     finally:
         if place is not None:
@@ -717,16 +718,15 @@ def kv4_read(cache, block_table, seq_lens, N, starts=None, dtype=None, k=None, v
 _KV4_WORKSPACES = {}
 
 
-def _kv4_workspace(device, sp, need):
-    import torch
+def _kv4_workspace(cache, sp, need):
     if torch._C._cuda_isCurrentStreamCapturing():
         # a graph has its own: it may be replayed on any stream, next to any other call
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    key = (device.index, sp)
+        return torch.empty(need, dtype=torch.uint8, device=cache.device)
+    key = (cache._index, sp)
     ws = _KV4_WORKSPACES.get(key)
     if ws is None or ws.shape[0] < need:
         # (made with that stream current: the memory of the old one goes back to its pool)
-        ws = _KV4_WORKSPACES[key] = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = _KV4_WORKSPACES[key] = torch.empty(need, dtype=torch.uint8, device=cache.device)
     return ws
 
 
@@ -743,21 +743,21 @@ def forward_kv4(q, cache, block_table, seq_lens, q_lens=None, causal=False, scal
     LSE = -inf. `workspace`: a uint8 tensor of at least attn_fwd_kv4_workspace_bytes(...);
     None: one kept per device and stream (inside a graph capture: the graph's own).
     Asynchronous like forward(); bad page numbers and lengths as in kv4_append."""
-    import torch
     B, Hq, N, dt = _kv4_rows(q, "q", cache)
-    bt, sl, max_pages = _kv4_tables(cache, block_table, seq_lens, B)
-    ql = None if q_lens is None else _kv4_int32(q_lens, "q_lens", (B,), cache.device)
+    bt, max_pages = _kv4_table(block_table, B, cache)
+    sl = _kv4_int32(seq_lens, "seq_lens", (B,), cache)
+    ql = None if q_lens is None else _kv4_int32(q_lens, "q_lens", (B,), cache)
     sp, place = _kv4_stream(cache, stream)
     try:
         if out is None:
             out = (torch.empty if q_lens is None else torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
-        else:
-            _kv4_like(out, "out", q)
+        o = _kv4_like(out, "out", q)
         if lse is None:
             if with_lse:
                 lse = (torch.empty if q_lens is None else torch.zeros)((B, Hq, N), dtype=torch.float32, device=q.device)
-        else:
-            _expect(lse, "lse", (B, Hq, N), torch.float32, q.device)
+        elif lse.dtype is not torch.float32 or lse.shape != (B, Hq, N) or lse.get_device() != cache._index or \
+                not lse.is_contiguous():
+            raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(B, Hq, N)} on {cache.device}")
         sizes = (B, Hq, N, max_pages)
         need = cache._need.get(sizes)
         if need is None:
@@ -765,17 +765,16 @@ def forward_kv4(q, cache, block_table, seq_lens, q_lens=None, causal=False, scal
                                                                      max_pages)
         if workspace is None:
             # (a shape the library refuses needs none: the call below says why)
-            workspace = _kv4_workspace(q.device, sp, need) if need else None
-        elif workspace.device != q.device or workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or \
-                workspace.numel() < need:
-            raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {q.device}")
-        _check(load().attn_fwd_kv4(q.data_ptr(), *cache._ptrs, bt, sl, ql, out.data_ptr(),
-                            None if lse is None else lse.data_ptr(),
-                            None if workspace is None else workspace.data_ptr(),
-                            0 if workspace is None else workspace.numel(), B, Hq, cache.heads, N, cache.d,
-                            cache.num_pages, cache.page_size, max_pages, cache.k_exp, cache.v_exp,
-                            0.0 if scale is None else float(scale), 1 if causal else 0, dt, sp), "attn_fwd_kv4")
-        if check:
+            workspace = _kv4_workspace(cache, sp, need) if need else None
+        elif workspace.get_device() != cache._index or workspace.dtype is not torch.uint8 or \
+                not workspace.is_contiguous() or workspace.numel() < need:
+            raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {cache.device}")
+        st = load().attn_fwd_kv4(cache._addr, q.data_ptr(), bt, sl, ql, o, None if lse is None else lse.data_ptr(),
+                                 None if workspace is None else workspace.data_ptr(),
+                                 0 if workspace is None else workspace.numel(), B, Hq, N, max_pages,
+                                 0.0 if scale is None else float(scale), 1 if causal else 0, dt, sp)
+        if st or check:
+            _check(st, "attn_fwd_kv4")
             _check_device(check, sp, "attn_fwd_kv4")
     finally:
         if place is not None:

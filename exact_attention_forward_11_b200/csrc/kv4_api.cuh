@@ -7,43 +7,40 @@ namespace {
 // the int32 arrays may be slices of larger ones
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-attn_status kv4_check_cache(const void* k_codes, const void* k_sf, const void* v_codes, const void* v_sf,
-                            const int* block_table, const int* seq_lens, int B, int Hkv, int N, int d, int num_pages,
-                            int page_size, int max_pages, int k_exp, int v_exp, int dtype) {
-  if (k_codes == nullptr || k_sf == nullptr || v_codes == nullptr || v_sf == nullptr || block_table == nullptr ||
-      seq_lens == nullptr)
+attn_status kv4_check_cache(const attn_kv4_cache* c, const int* block_table, const int* seq_lens, int B, int N,
+                            int max_pages, int dtype) {
+  if (c == nullptr || c->k_codes == nullptr || c->k_sf == nullptr || c->v_codes == nullptr || c->v_sf == nullptr ||
+      block_table == nullptr || seq_lens == nullptr)
     return ATTN_ERR_INVALID_ARG;
-  if (attn_status s = check_shape(B, Hkv, N); s != ATTN_OK) return s;
-  if (num_pages < 1 || max_pages < 1 || page_size < 1) return ATTN_ERR_INVALID_ARG;
-  if (k_exp < -32 || k_exp > 32 || v_exp < -32 || v_exp > 32) return ATTN_ERR_INVALID_ARG;
-  if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(max_pages) * page_size >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
-  if (static_cast<long long>(num_pages) * Hkv >= (1ll << 32) / page_size) return ATTN_ERR_INVALID_ARG;
+  if (attn_status s = check_shape(B, c->Hkv, N); s != ATTN_OK) return s;
+  if (c->num_pages < 1 || max_pages < 1 || c->page_size < 1) return ATTN_ERR_INVALID_ARG;
+  if (c->k_exp < -32 || c->k_exp > 32 || c->v_exp < -32 || c->v_exp > 32) return ATTN_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)) != 0) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_pages) * c->page_size >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(c->num_pages) * c->Hkv >= (1ll << 32) / c->page_size) return ATTN_ERR_INVALID_ARG;
   if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_UNSUPPORTED;
-  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
-  if (!aligned16(k_codes) || !aligned16(k_sf) || !aligned16(v_codes) || !aligned16(v_sf) || !aligned4(block_table) ||
-      !aligned4(seq_lens))
+  if (c->d != 64 && c->d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(c->k_codes) || !aligned16(c->k_sf) || !aligned16(c->v_codes) || !aligned16(c->v_sf) ||
+      !aligned4(block_table) || !aligned4(seq_lens))
     return ATTN_ERR_MISALIGNED;
   return ATTN_OK;
 }
 
-attn::Kv4Cache kv4_cache_of(const void* k_codes, const void* k_sf, const void* v_codes, const void* v_sf,
-                            const int* block_table, const int* seq_lens, int B, int Hkv, int num_pages, int page_size,
-                            int max_pages, int k_exp, int v_exp) {
+attn::Kv4Cache kv4_cache_of(const attn_kv4_cache* from, const int* block_table, const int* seq_lens, int B, int max_pages) {
   attn::Kv4Cache c;
-  c.codes[0] = static_cast<uint8_t*>(const_cast<void*>(k_codes));
-  c.codes[1] = static_cast<uint8_t*>(const_cast<void*>(v_codes));
-  c.sf[0] = static_cast<uint8_t*>(const_cast<void*>(k_sf));
-  c.sf[1] = static_cast<uint8_t*>(const_cast<void*>(v_sf));
+  c.codes[0] = static_cast<uint8_t*>(from->k_codes);
+  c.codes[1] = static_cast<uint8_t*>(from->v_codes);
+  c.sf[0] = static_cast<uint8_t*>(from->k_sf);
+  c.sf[1] = static_cast<uint8_t*>(from->v_sf);
   c.block_table = block_table;
   c.seq_lens = seq_lens;
   c.B = B;
-  c.H = Hkv;
-  c.num_pages = num_pages;
-  c.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
+  c.H = from->Hkv;
+  c.num_pages = from->num_pages;
+  c.page_shift = __builtin_ctz(static_cast<unsigned>(from->page_size));
   c.max_pages = max_pages;
-  c.exp[0] = k_exp;
-  c.exp[1] = v_exp;
+  c.exp[0] = from->k_exp;
+  c.exp[1] = from->v_exp;
   return c;
 }
 
@@ -134,51 +131,44 @@ attn_status launch_kv4_rows(const attn::Kv4AttnParams& p, const Kv4Plan& plan, c
 
 extern "C" {
 
-attn_status attn_kv4_append(const void* k, const void* v, void* k_codes, void* k_sf, void* v_codes, void* v_sf,
-                            const int* block_table, const int* seq_lens, const int* new_lens, int B, int Hkv, int N,
-                            int d, int num_pages, int page_size, int max_pages, int k_exp, int v_exp,
-                            attn_dtype dtype, void* stream) {
+attn_status attn_kv4_append(const attn_kv4_cache* cache, const void* k, const void* v, const int* block_table,
+                            const int* seq_lens, const int* new_lens, int B, int N, int max_pages, attn_dtype dtype,
+                            void* stream) {
   if (k == nullptr || v == nullptr) return ATTN_ERR_INVALID_ARG;
-  if (attn_status s = kv4_check_cache(k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, B, Hkv, N, d, num_pages,
-                                      page_size, max_pages, k_exp, v_exp, dtype);
-      s != ATTN_OK)
-    return s;
+  if (attn_status s = kv4_check_cache(cache, block_table, seq_lens, B, N, max_pages, dtype); s != ATTN_OK) return s;
   if (!aligned16(k) || !aligned16(v) || !aligned4(new_lens)) return ATTN_ERR_MISALIGNED;
   attn::Kv4MoveParams p{};
-  p.c = kv4_cache_of(k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, B, Hkv, num_pages, page_size, max_pages,
-                     k_exp, v_exp);
+  p.c = kv4_cache_of(cache, block_table, seq_lens, B, max_pages);
   p.in[0] = static_cast<const uint8_t*>(k);
   p.in[1] = static_cast<const uint8_t*>(v);
   p.first = new_lens;
   p.N = N;
   p.tiles = (N + attn::kKv4Rows - 1) / attn::kKv4Rows;
-  auto kern = d == 128 ? (dtype == ATTN_FP16 ? attn::kv4_append_sm100<128, true> : attn::kv4_append_sm100<128, false>)
-                       : (dtype == ATTN_FP16 ? attn::kv4_append_sm100<64, true> : attn::kv4_append_sm100<64, false>);
-  kern<<<dim3(static_cast<unsigned>(B * Hkv * p.tiles), 2), attn::kKv4Threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  const bool f16 = dtype == ATTN_FP16;
+  auto kern = cache->d == 128 ? (f16 ? attn::kv4_append_sm100<128, true> : attn::kv4_append_sm100<128, false>)
+                              : (f16 ? attn::kv4_append_sm100<64, true> : attn::kv4_append_sm100<64, false>);
+  kern<<<dim3(static_cast<unsigned>(B * cache->Hkv * p.tiles), 2), attn::kKv4Threads, 0,
+         static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-attn_status attn_kv4_read(const void* k_codes, const void* k_sf, const void* v_codes, const void* v_sf,
-                          const int* block_table, const int* seq_lens, const int* starts, void* k, void* v, int B,
-                          int Hkv, int N, int d, int num_pages, int page_size, int max_pages, int k_exp, int v_exp,
-                          attn_dtype dtype, void* stream) {
+attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block_table, const int* seq_lens, const int* starts,
+                          void* k, void* v, int B, int N, int max_pages, attn_dtype dtype, void* stream) {
   if (k == nullptr || v == nullptr) return ATTN_ERR_INVALID_ARG;
-  if (attn_status s = kv4_check_cache(k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, B, Hkv, N, d, num_pages,
-                                      page_size, max_pages, k_exp, v_exp, dtype);
-      s != ATTN_OK)
-    return s;
+  if (attn_status s = kv4_check_cache(cache, block_table, seq_lens, B, N, max_pages, dtype); s != ATTN_OK) return s;
   if (!aligned16(k) || !aligned16(v) || !aligned4(starts)) return ATTN_ERR_MISALIGNED;
   attn::Kv4MoveParams p{};
-  p.c = kv4_cache_of(k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, B, Hkv, num_pages, page_size, max_pages,
-                     k_exp, v_exp);
+  p.c = kv4_cache_of(cache, block_table, seq_lens, B, max_pages);
   p.out[0] = static_cast<uint8_t*>(k);
   p.out[1] = static_cast<uint8_t*>(v);
   p.first = starts;
   p.N = N;
   p.tiles = (N + attn::kKv4Rows - 1) / attn::kKv4Rows;
-  auto kern = d == 128 ? (dtype == ATTN_FP16 ? attn::kv4_read_sm100<128, true> : attn::kv4_read_sm100<128, false>)
-                       : (dtype == ATTN_FP16 ? attn::kv4_read_sm100<64, true> : attn::kv4_read_sm100<64, false>);
-  kern<<<dim3(static_cast<unsigned>(B * Hkv * p.tiles), 2), attn::kKv4Threads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  const bool f16 = dtype == ATTN_FP16;
+  auto kern = cache->d == 128 ? (f16 ? attn::kv4_read_sm100<128, true> : attn::kv4_read_sm100<128, false>)
+                              : (f16 ? attn::kv4_read_sm100<64, true> : attn::kv4_read_sm100<64, false>);
+  kern<<<dim3(static_cast<unsigned>(B * cache->Hkv * p.tiles), 2), attn::kKv4Threads, 0,
+         static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -188,27 +178,22 @@ size_t attn_fwd_kv4_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int pa
   return kv4_plan(B, Hq, Hkv, N, d, page_size, max_pages).workspace;
 }
 
-attn_status attn_fwd_kv4(const void* q, const void* k_codes, const void* k_sf, const void* v_codes, const void* v_sf,
-                         const int* block_table, const int* seq_lens, const int* q_lens, void* o, float* lse,
-                         void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int N, int d, int num_pages,
-                         int page_size, int max_pages, int k_exp, int v_exp, float scale, int causal,
-                         attn_dtype dtype, void* stream) {
-  if (q == nullptr || o == nullptr) return ATTN_ERR_INVALID_ARG;
+attn_status attn_fwd_kv4(const attn_kv4_cache* cache, const void* q, const int* block_table, const int* seq_lens,
+                         const int* q_lens, void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int Hq,
+                         int N, int max_pages, float scale, int causal, attn_dtype dtype, void* stream) {
+  if (q == nullptr || o == nullptr || cache == nullptr) return ATTN_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+  const int d = cache->d, Hkv = cache->Hkv;
   if (attn_status s = resolve_scale(scale, d > 0 ? d : 1); s != ATTN_OK) return s;
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
   if (attn_status s = check_shape(B, Hq, N); s != ATTN_OK) return s;
-  if (attn_status s = kv4_check_cache(k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, B, Hkv, N, d, num_pages,
-                                      page_size, max_pages, k_exp, v_exp, dtype);
-      s != ATTN_OK)
-    return s;
-  const size_t need = attn_fwd_kv4_workspace_bytes(B, Hq, Hkv, N, d, page_size, max_pages);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
+  if (attn_status s = kv4_check_cache(cache, block_table, seq_lens, B, N, max_pages, dtype); s != ATTN_OK) return s;
+  const Kv4Plan plan = kv4_plan(B, Hq, Hkv, N, d, cache->page_size, max_pages);
+  if (workspace == nullptr || workspace_bytes < plan.workspace) return ATTN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned4(q_lens) || !aligned16(workspace))
     return ATTN_ERR_MISALIGNED;
   attn::Kv4AttnParams p{};
-  p.c = kv4_cache_of(k_codes, k_sf, v_codes, v_sf, block_table, seq_lens, B, Hkv, num_pages, page_size, max_pages,
-                     k_exp, v_exp);
+  p.c = kv4_cache_of(cache, block_table, seq_lens, B, max_pages);
   p.q = static_cast<const uint8_t*>(q);
   p.o = static_cast<uint8_t*>(o);
   p.lse = lse;
@@ -216,8 +201,7 @@ attn_status attn_fwd_kv4(const void* q, const void* k_codes, const void* k_sf, c
   p.Hq = Hq;
   p.N = N;
   p.causal = causal;
-  p.scale_log2 = std::ldexp(scale * 1.4426950408889634f, k_exp);
-  const Kv4Plan plan = kv4_plan(B, Hq, Hkv, N, d, page_size, max_pages);
+  p.scale_log2 = std::ldexp(scale * 1.4426950408889634f, cache->k_exp);
   p.row_blocks = plan.row_blocks;
   p.ctas = plan.ctas;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -53,6 +53,16 @@
 extern "C" {
 #endif
 
+/* A cache: its tensors and sizes, as every call takes them (a host struct, read during the call). */
+typedef struct {
+  void* k_codes;             /* device pointers */
+  void* k_sf;
+  void* v_codes;
+  void* v_sf;
+  int num_pages, page_size, Hkv, d;
+  int k_exp, v_exp;
+} attn_kv4_cache;
+
 /*
  * attn_kv4_append - quantises new keys and values into the cache.
  *   k, v     : [B, Hkv, N, d] new tokens of each sequence.
@@ -62,10 +72,9 @@ extern "C" {
  *              tokens each; rows behind new_lens[b] are ignored.
  * Two sequences must not append to the same page slot in one call.
  */
-ATTN_API attn_status attn_kv4_append(const void* k, const void* v, void* k_codes, void* k_sf, void* v_codes,
-                                     void* v_sf, const int* block_table, const int* seq_lens, const int* new_lens,
-                                     int B, int Hkv, int N, int d, int num_pages, int page_size, int max_pages,
-                                     int k_exp, int v_exp, attn_dtype dtype, void* stream);
+ATTN_API attn_status attn_kv4_append(const attn_kv4_cache* cache, const void* k, const void* v, const int* block_table,
+                                     const int* seq_lens, const int* new_lens, int B, int N, int max_pages,
+                                     attn_dtype dtype, void* stream);
 
 /*
  * attn_kv4_read - reads positions back.
@@ -74,10 +83,9 @@ ATTN_API attn_status attn_kv4_append(const void* k, const void* v, void* k_codes
  *            or behind seq_lens[b] are written as zeros.
  *   starts : [B] int32, 0 or more, or NULL for 0.
  */
-ATTN_API attn_status attn_kv4_read(const void* k_codes, const void* k_sf, const void* v_codes, const void* v_sf,
-                                   const int* block_table, const int* seq_lens, const int* starts, void* k, void* v,
-                                   int B, int Hkv, int N, int d, int num_pages, int page_size, int max_pages,
-                                   int k_exp, int v_exp, attn_dtype dtype, void* stream);
+ATTN_API attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block_table, const int* seq_lens,
+                                   const int* starts, void* k, void* v, int B, int N, int max_pages,
+                                   attn_dtype dtype, void* stream);
 
 /*
  * attn_fwd_kv4 - attention of queries over the cache.
@@ -100,11 +108,10 @@ ATTN_API attn_status attn_kv4_read(const void* k_codes, const void* k_sf, const 
  * f16, P is rounded to f16); softmax statistics in fp32. Repeated calls give
  * bit-identical results.
  */
-ATTN_API attn_status attn_fwd_kv4(const void* q, const void* k_codes, const void* k_sf, const void* v_codes,
-                                  const void* v_sf, const int* block_table, const int* seq_lens, const int* q_lens,
-                                  void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int Hq,
-                                  int Hkv, int N, int d, int num_pages, int page_size, int max_pages, int k_exp,
-                                  int v_exp, float scale, int causal, attn_dtype dtype, void* stream);
+ATTN_API attn_status attn_fwd_kv4(const attn_kv4_cache* cache, const void* q, const int* block_table,
+                                  const int* seq_lens, const int* q_lens, void* o, float* lse, void* workspace,
+                                  size_t workspace_bytes, int B, int Hq, int N, int max_pages, float scale, int causal,
+                                  attn_dtype dtype, void* stream);
 
 /* attn_fwd_kv4_workspace_bytes - workspace attn_fwd_kv4 needs for this shape (0 also for
  * an invalid or unsupported one). Host only; launches nothing. */

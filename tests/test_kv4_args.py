@@ -1,4 +1,6 @@
 """The 4-bit cache calls refuse bad arguments on the host, before any CUDA call (CPU)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -14,35 +16,45 @@ def lib():
     return attn
 
 
-MOVE = dict(a=FAKE, b=FAKE, c=FAKE, d_=FAKE, e=FAKE, f=FAKE, g=FAKE, h=FAKE, i=None, B=1, Hkv=2, N=3, d=128, pages=4,
-            page=16, maxp=2, ke=0, ve=0, dtype=0, stream=None)
-FWD = dict(q=FAKE, kc=FAKE, ks=FAKE, vc=FAKE, vs=FAKE, bt=FAKE, sl=FAKE, ql=None, o=FAKE, lse=None, ws=FAKE,
-           wsb=1 << 40, B=1, Hq=4, Hkv=2, N=3, d=128, pages=4, page=16, maxp=2, ke=0, ve=0, scale=0.0, causal=0,
-           dtype=0, stream=None)
+CACHE = dict(k_codes=FAKE, k_sf=FAKE, v_codes=FAKE, v_sf=FAKE, num_pages=4, page_size=16, Hkv=2, d=128, k_exp=0, v_exp=0)
+MOVE = dict(k=FAKE, v=FAKE, bt=FAKE, sl=FAKE, first=None, B=1, N=3, maxp=2, dtype=0, stream=None)
+FWD = dict(q=FAKE, bt=FAKE, sl=FAKE, ql=None, o=FAKE, lse=None, ws=FAKE, wsb=1 << 40, B=1, Hq=4, N=3, maxp=2, scale=0.0,
+           causal=0, dtype=0, stream=None)
+
+
+def split(args, change):
+    """(address of a cache struct, the other arguments by name) with the changes of either made."""
+    struct = attn.attn_kv4_cache(**{k: change.get(k, v) for k, v in CACHE.items()})
+    split.kept = struct                                        # alive during the call
+    addr = None if "cache" in change else ctypes.addressof(struct)
+    return addr, {k: change.get(k, v) for k, v in args.items()}
+
+
 # (changed arguments, status) that all three calls share
-SHARED = [(dict(B=0), 1), (dict(Hkv=0), 1), (dict(N=-1), 1), (dict(pages=0), 1), (dict(maxp=0), 1), (dict(page=0), 1),
-          (dict(page=24), 2), (dict(page=8), 2), (dict(page=1 << 17), 2), (dict(d=96), 2), (dict(d=256), 2), (dict(dtype=2), 2),
-          (dict(ke=33), 1), (dict(ve=-33), 1), (dict(page=65536, maxp=1 << 15), 1),
-          (dict(pages=1 << 30, page=16), 1)]
+SHARED = [(dict(cache=None), 1), (dict(k_codes=None), 1), (dict(v_sf=None), 1), (dict(bt=None), 1), (dict(sl=None), 1),
+          (dict(B=0), 1), (dict(Hkv=0), 1), (dict(N=-1), 1), (dict(num_pages=0), 1), (dict(maxp=0), 1),
+          (dict(page_size=0), 1), (dict(page_size=24), 2), (dict(page_size=8), 2), (dict(page_size=1 << 17), 2),
+          (dict(d=96), 2), (dict(d=256), 2), (dict(dtype=2), 2), (dict(k_exp=33), 1), (dict(v_exp=-33), 1),
+          (dict(page_size=65536, maxp=1 << 15), 1), (dict(num_pages=1 << 30), 1), (dict(B=1 << 16, N=1 << 15), 1),
+          (dict(k_codes=FAKE + 2), 3), (dict(v_sf=FAKE + 8), 3), (dict(bt=FAKE + 2), 3), (dict(sl=FAKE + 1), 3)]
 
 
 @pytest.mark.parametrize("change,status", SHARED + [
-    (dict(a=None), 1), (dict(c=None), 1), (dict(g=None), 1), (dict(h=None), 1), (dict(a=FAKE + 8), 3),
-    (dict(c=FAKE + 2), 3), (dict(i=FAKE + 2), 3), (dict(B=1 << 16, N=1 << 15), 1)])
+    (dict(k=None), 1), (dict(v=None), 1), (dict(k=FAKE + 8), 3), (dict(first=FAKE + 2), 3)])
 def test_append_and_read_refuse(lib, change, status):
-    args = list(dict(MOVE, **change).values())
-    assert lib.attn_kv4_append(*args) == status                # k, v, caches, tables, new_lens, ...
-    order = args[2:8] + [args[8], args[0], args[1]] + args[9:]  # caches, tables, starts, k, v, ...
-    assert lib.attn_kv4_read(*order) == status
+    addr, a = split(MOVE, change)
+    rest = (a["B"], a["N"], a["maxp"], a["dtype"], a["stream"])
+    assert lib.attn_kv4_append(addr, a["k"], a["v"], a["bt"], a["sl"], a["first"], *rest) == status
+    assert lib.attn_kv4_read(addr, a["bt"], a["sl"], a["first"], a["k"], a["v"], *rest) == status
 
 
 @pytest.mark.parametrize("change,status", SHARED + [
-    (dict(q=None), 1), (dict(o=None), 1), (dict(kc=None), 1), (dict(vs=None), 1), (dict(bt=None), 1), (dict(sl=None), 1),
-    (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(causal=2), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
-    (dict(q=FAKE + 4), 3), (dict(lse=FAKE + 4), 3), (dict(ql=FAKE + 1), 3), (dict(vs=FAKE + 8), 3), (dict(ws=FAKE + 8), 3),
-    (dict(B=1 << 16, N=1 << 15), 1)])
+    (dict(q=None), 1), (dict(o=None), 1), (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(causal=2), 1), (dict(scale=-1.0), 1),
+    (dict(scale=float("nan")), 1), (dict(q=FAKE + 4), 3), (dict(lse=FAKE + 4), 3), (dict(ql=FAKE + 1), 3),
+    (dict(ws=FAKE + 8), 3)])
 def test_forward_refuses(lib, change, status):
-    assert lib.attn_fwd_kv4(*dict(FWD, **change).values()) == status
+    addr, a = split(FWD, change)
+    assert lib.attn_fwd_kv4(addr, *a.values()) == status
 
 
 def test_workspace_bytes_and_a_small_workspace(lib):
@@ -51,9 +63,9 @@ def test_workspace_bytes_and_a_small_workspace(lib):
                 (1, 4, 2, 1, 128, 24, 64), (1, 4, 2, 1, 128, 16, 0)):
         assert wsb(*bad) == 0
     need = wsb(1, 4, 2, 3, 128, 16, 2)
-    if need:
-        assert lib.attn_fwd_kv4(*dict(FWD, wsb=need - 1).values()) == 1
-        assert lib.attn_fwd_kv4(*dict(FWD, ws=None).values()) == 1
+    for change in (dict(wsb=need - 1), dict(ws=None)):
+        addr, a = split(FWD, change)
+        assert lib.attn_fwd_kv4(addr, *a.values()) == 1
 
 
 def test_binding_refuses_tensors():
