@@ -3,9 +3,8 @@
 // (include/kv4_b200.h gives the definition).
 //
 // A row is one token of one head: d / 2 bytes of E2M1 codes and d / 16 E4M3 scale
-// bytes. Both kernels move bytes and little else: a thread takes one block of 16
-// values (32 bytes of 16-bit values, 8 bytes of codes, one scale byte), so a warp
-// reads or writes 1 KB of consecutive values.
+// bytes. Both kernels move bytes and little else: a CTA takes 64 rows of one head
+// (of one tensor), its lanes consecutive pieces of a row.
 #pragma once
 
 #include <cstdint>
@@ -135,95 +134,107 @@ __device__ __forceinline__ uint32_t kv4_lookup(const Kv4MoveParams& p, int b, in
   return kv4_row(p.c, page, h, pos, row) ? row : kNoRow;
 }
 
-// Quantises new tokens: a thread takes one block of 16 values of each of its rows. A quotient y / s decides
-// a code only by its side of a border of E2M1 (t = 0.25 ... 5). It is taken as y * (1 / s) rounded to 16
-// significant bits, which decides alike: y has at most 11 bits and t s at most 7, so y / s is t itself or a
-// relative 2^-11 away from it; y * (1 / s) is off by at most 2^-23, and rounding to 16 bits (2^-17) takes
-// an exact t (3 bits) back to t and moves nothing across it. (Sixteen IEEE divisions a block instead: 50.8
-// against 45 us on append_prompt, with its read.)
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// In both kernels a warp moves 8 rows: LPR lanes hold a row, 32 / LPR rows make a pass, and one lane looks up
+// each of the 8 rows. Both are near the bytes they move, and instructions are what is left: with every lane
+// looking up its own row, and quotients rounded in integers, append_prompt (4 x 8 heads x 4096 tokens written
+// and read back) took 38.0 us instead of 34.1 and read_long (8 heads x 32768 tokens) 32.2 instead of 30.6.
+constexpr int kKv4WarpRows = kKv4Rows / (kKv4Threads / 32);
+static_assert(kKv4WarpRows == 8, "rows of a warp");
+
+// Quantises new tokens: a thread takes one block of 16 values of each of its rows. A quotient q = y / s
+// decides a code only by its side of a border of E2M1 (t = 0.25 ... 5). It is taken as y * (1 / s) rounded to
+// a multiple of 2^-16 by adding and subtracting 192, which decides alike: y has at most 11 significant bits and
+// t s at most 7, so q is t itself or at least 2^-11 t >= 2^-13 away from it; 1 / s is off by 2^-24 of
+// itself and the sum rounds by 2^-17, so an exact t comes out as t and nothing crosses one. (Sixteen IEEE
+// divisions a block took 2 us more on append_prompt.)
 template <int D, bool F16>
 __global__ void __launch_bounds__(kKv4Threads) kv4_append_sm100(const __grid_constant__ Kv4MoveParams p) {
-  constexpr int BLK = D / 16, PASS = kKv4Threads / BLK, U = kKv4Rows / PASS;   // rows per pass, passes
-  const int which = blockIdx.y, blk = threadIdx.x % BLK;
-  const float down = f32_exp2i(-p.c.exp[which]);
+  constexpr int LPR = D / 16, RPP = 32 / LPR, U = kKv4WarpRows / RPP;   // lanes per row, rows per pass, passes
+  const int which = blockIdx.y, lane = threadIdx.x & 31, blk = lane % LPR;
+  const int exp2 = which == 0 ? p.c.exp[0] : p.c.exp[1];
   const Kv4MoveTile tile(p);
-  const uint4* src = reinterpret_cast<const uint4*>(p.in[which]) + tile.row0 * (BLK * 2) + blk * 2;
+  const int r0 = (threadIdx.x >> 5) * kKv4WarpRows;                     // the warp's first row of the tile
+  const uint4* src = reinterpret_cast<const uint4*>(which == 0 ? p.in[0] : p.in[1]) + tile.row0 * (LPR * 2) + blk * 2;
   uint4 x[U][2];
 #pragma unroll
   for (int j = 0; j < U; ++j) {
-    const int r = j * PASS + threadIdx.x / BLK;
+    const int r = r0 + j * RPP + lane / LPR;
     if (tile.i0 + r < p.N) {
-      x[j][0] = __ldg(src + r * (BLK * 2));
-      x[j][1] = __ldg(src + r * (BLK * 2) + 1);
+      x[j][0] = __ldg(src + r * (LPR * 2));
+      x[j][1] = __ldg(src + r * (LPR * 2) + 1);
     }
   }
   const int len = kv4_len(p.c, tile.b), n = p.first != nullptr ? kv4_clamp(p.first[tile.b], p.N) : p.N;
   if (n > len) kv4_record(static_cast<unsigned long long>(static_cast<long long>(len - n)));   // tokens before position 0
-  uint32_t row[U];
+  const int mine = tile.i0 + r0 + (lane & 7);
+  const uint32_t my_row = kv4_lookup(p, tile.b, tile.h, lane < 8 && mine < n ? len - n + mine : -1);
+  uint8_t* const codes = (which == 0 ? p.c.codes[0] : p.c.codes[1]) + blk * 8;
+  uint8_t* const sf = (which == 0 ? p.c.sf[0] : p.c.sf[1]) + blk;
 #pragma unroll
   for (int j = 0; j < U; ++j) {
-    const int i = tile.i0 + j * PASS + threadIdx.x / BLK;
-    row[j] = kv4_lookup(p, tile.b, tile.h, i < n ? len - n + i : -1);
-  }
-#pragma unroll
-  for (int j = 0; j < U; ++j) {
-    if (row[j] == kNoRow) continue;
+    const uint32_t row = __shfl_sync(0xffffffffu, my_row, j * RPP + lane / LPR);
+    if (row == kNoRow) continue;
     const uint32_t w[8] = {x[j][0].x, x[j][0].y, x[j][0].z, x[j][0].w, x[j][1].x, x[j][1].y, x[j][1].z, x[j][1].w};
     float v[16];
     float amax = 0.f;
-    bool nan = false;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float2 f = f32x2_from_16<F16>(w[k]);
-      v[2 * k] = f.x * down;
-      v[2 * k + 1] = f.y * down;
-      amax = fmaxf(amax, fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
-      nan = nan || f.x != f.x || f.y != f.y;
+      v[2 * k] = f.x;
+      v[2 * k + 1] = f.y;
+      amax = max_nan(amax, max_nan(fabsf(f.x), fabsf(f.y)));
     }
-    const float want = fminf(fmaxf(__fdiv_rn(amax, 6.f), 0.001953125f), 448.f);
+    const bool nan = amax != amax;
+    const float down = f32_exp2i(-exp2);
+    const float want = fminf(fmaxf(__fdiv_rn(amax * down, 6.f), 0.001953125f), 448.f);
     const uint32_t byte = b200::pack_e4m3x4(want, 0.f, 0.f, 0.f) & 0xFFu;
-    const float inv = __frcp_rn(f32x2_from_f16x2(b200::f16x2_from_e4m3x2(static_cast<uint16_t>(byte))).x);
+    const float inv = __frcp_rn(f32x2_from_f16x2(b200::f16x2_from_e4m3x2(static_cast<uint16_t>(byte))).x) * down;
     uint32_t out[2] = {0u, 0u};
-    if (!nan) {
-      auto quotient = [&](float y) {                 // 16 significant bits, rounded half away from zero
-        return __uint_as_float((__float_as_uint(y * inv) + 0x80u) & 0xFFFFFF00u);
-      };
+    auto quotient = [&](float y) { return __fsub_rn(__fmaf_rn(y, inv, 192.f), 192.f); };
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        out[k >> 2] |= e2m1x2_from_f32(quotient(v[2 * k]), quotient(v[2 * k + 1])) << (8 * (k & 3));
-    }
-    *reinterpret_cast<uint2*>(p.c.codes[which] + static_cast<size_t>(row[j]) * (D / 2) + blk * 8) = make_uint2(out[0], out[1]);
-    p.c.sf[which][static_cast<size_t>(row[j]) * BLK + blk] = static_cast<uint8_t>(nan ? 0x7Fu : byte);
+    for (int k = 0; k < 8; ++k)
+      out[k >> 2] |= e2m1x2_from_f32(quotient(v[2 * k]), quotient(v[2 * k + 1])) << (8 * (k & 3));
+    if (nan) out[0] = out[1] = 0u;
+    *reinterpret_cast<uint2*>(codes + static_cast<size_t>(row) * (D / 2)) = make_uint2(out[0], out[1]);
+    sf[static_cast<size_t>(row) * LPR] = static_cast<uint8_t>(nan ? 0x7Fu : byte);
   }
 }
 
 // Reads positions back: a thread takes 8 values (4 bytes of codes, one 16-byte store) of each of its rows.
 template <int D, bool F16>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_sm100(const __grid_constant__ Kv4MoveParams p) {
-  constexpr int UPR = D / 8, PASS = kKv4Threads / UPR, U = kKv4Rows / PASS;
-  const int which = blockIdx.y, unit = threadIdx.x % UPR;
-  const float up = f32_exp2i(p.c.exp[which]);
+  constexpr int LPR = D / 8, RPP = 32 / LPR, U = kKv4WarpRows / RPP;
+  const int which = blockIdx.y, lane = threadIdx.x & 31, unit = lane % LPR;
+  const float up = f32_exp2i(which == 0 ? p.c.exp[0] : p.c.exp[1]);
   const Kv4MoveTile tile(p);
+  const int r0 = (threadIdx.x >> 5) * kKv4WarpRows;
   const int start = p.first != nullptr ? kv4_clamp(p.first[tile.b], p.c.max_pages << p.c.page_shift) : 0;
   const int rows = kv4_len(p.c, tile.b) - start;     // rows that hold a position
-  uint32_t row[U], w[U], byte[U];
+  const int mine = tile.i0 + r0 + (lane & 7);
+  const uint32_t my_row = kv4_lookup(p, tile.b, tile.h, lane < 8 && mine < rows && mine < p.N ? start + mine : -1);
+  const uint8_t* const codes = (which == 0 ? p.c.codes[0] : p.c.codes[1]) + unit * 4;
+  const uint8_t* const sf = (which == 0 ? p.c.sf[0] : p.c.sf[1]) + (unit >> 1);
+  uint32_t w[U], byte[U];
 #pragma unroll
   for (int j = 0; j < U; ++j) {
-    const int i = tile.i0 + j * PASS + threadIdx.x / UPR;
-    row[j] = kv4_lookup(p, tile.b, tile.h, i < rows && i < p.N ? start + i : -1);
-  }
-#pragma unroll
-  for (int j = 0; j < U; ++j) {
+    const uint32_t row = __shfl_sync(0xffffffffu, my_row, j * RPP + lane / LPR);
     w[j] = byte[j] = 0u;
-    if (row[j] != kNoRow) {
-      w[j] = __ldg(reinterpret_cast<const uint32_t*>(p.c.codes[which] + static_cast<size_t>(row[j]) * (D / 2)) + unit);
-      byte[j] = __ldg(p.c.sf[which] + static_cast<size_t>(row[j]) * (D / 16) + (unit >> 1));
+    if (row != kNoRow) {
+      w[j] = __ldg(reinterpret_cast<const uint32_t*>(codes + static_cast<size_t>(row) * (D / 2)));
+      byte[j] = __ldg(sf + static_cast<size_t>(row) * (D / 16));
     }
   }
-  uint4* dst = reinterpret_cast<uint4*>(p.out[which]) + tile.row0 * UPR + unit;
+  uint4* dst = reinterpret_cast<uint4*>(which == 0 ? p.out[0] : p.out[1]) + tile.row0 * LPR + unit;
 #pragma unroll
   for (int j = 0; j < U; ++j) {
-    const int r = j * PASS + threadIdx.x / UPR;
+    const int r = r0 + j * RPP + lane / LPR;
     if (tile.i0 + r >= p.N) break;
     const uint32_t s2 = b200::f16x2_from_e4m3x2(static_cast<uint16_t>(byte[j] | (byte[j] << 8)));
     uint32_t f[4], out[4];
@@ -233,7 +244,7 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_sm100(const __grid_const
       const float2 a = f32x2_from_f16x2(hmul2(f[k], s2));
       out[k] = pack_16<F16>(a.x * up, a.y * up);
     }
-    dst[r * UPR] = make_uint4(out[0], out[1], out[2], out[3]);
+    dst[r * LPR] = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 

@@ -17,6 +17,7 @@ So with A = sum_j p_j |v_j| / l:
 with ds' = ds + 2^-22 max|S|.
 """
 import math
+import os
 
 import numpy as np
 import pytest
@@ -491,3 +492,52 @@ def test_many_sequences(cuda_lib, N):
     o, lse = lib.forward_kv4(big, pg.cache, pg.bt, ints(lens), q_lens=ints([min(150, x) for x in lens]), causal=True,
                              check=True)
     check_attention(o, lse, big, pg, lens, [min(150, x) for x in lens], True, rows=(0, 1, 40, 149))
+
+
+def test_debug_build_is_bit_identical(cuda_lib):
+    """The debug build's cache calls give the release build's bits, and report a bad page with its site."""
+    lib, d = cuda_lib, 128
+    from exact_attention_forward_11_b200 import build
+    assert os.path.exists(build.build(debug=True))
+    lens = [400, 77]
+    pg = Paged(lib, 2, 2, d, 16, 25, seed=4)
+    k, v = fill(pg, lens, torch.bfloat16, 2)
+    qs = [make_q(2, 4, N, d, torch.bfloat16, N) for N in (1, 7, 40, 150)]
+    want = [lib.forward_kv4(q, pg.cache, pg.bt, ints(lens), causal=True, check=True) for q in qs]
+    codes = [t.clone() for t in pg.tensors()]
+    read = lib.kv4_read(pg.cache, pg.bt, ints(lens), 300, check=True)
+    prev = lib.use_library(lib.DEBUG_LIB_PATH)
+    try:
+        assert lib.attn_debug_build() == 1
+        lib.kv4_append(pg.cache, k, v, pg.bt, ints(lens), new_lens=ints(lens), check=True)
+        assert all(torch.equal(a, b) for a, b in zip(codes, pg.tensors()))
+        assert all(torch.equal(a, b) for a, b in zip(read, lib.kv4_read(pg.cache, pg.bt, ints(lens), 300, check=True)))
+        for q, w in zip(qs, want):
+            o, lse = lib.forward_kv4(q, pg.cache, pg.bt, ints(lens), causal=True, check=True)
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+        bad = pg.bt.clone()
+        bad[1, 1] = 12345678
+        lib.forward_kv4(qs[0], pg.cache, bad, ints(lens))
+        torch.cuda.synchronize()
+        assert lib.attn_get_device_status(None) == lib.ATTN_ERR_BOUNDS
+        assert lib.attn_debug_last_failure(None) == (12, 12345678)
+    finally:
+        lib.use_library(prev)
+
+
+def test_offset_tables_and_odd_strides(cuda_lib):
+    """int32 arguments that are slices of larger arrays (4-byte aligned), and a refused non-contiguous one."""
+    lib, d = cuda_lib, 64
+    lens = [33, 250, 90]
+    pg = Paged(lib, 3, 2, d, 16, 16, seed=4)
+    fill(pg, lens, torch.float16, 2)
+    q = make_q(3, 2, 2, d, torch.float16, 1)
+    want = lib.forward_kv4(q, pg.cache, pg.bt, ints(lens), q_lens=ints([2, 1, 2]), causal=True, check=True)
+    sl, ql = ints([9] + lens)[1:], ints([9, 9, 9, 2, 1, 2])[3:]
+    bt = torch.cat([pg.bt.new_zeros(1), pg.bt.view(-1)])[1:].view_as(pg.bt)
+    got = lib.forward_kv4(q, pg.cache, bt, sl, q_lens=ql, causal=True, check=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(ValueError):
+        lib.forward_kv4(q, pg.cache, pg.bt.t().contiguous().t(), ints(lens))
+    with pytest.raises(ValueError):
+        lib.forward_kv4(q, pg.cache, pg.bt, torch.stack([ints(lens), ints(lens)], 1)[:, 0])
