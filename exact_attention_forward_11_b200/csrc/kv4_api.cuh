@@ -52,9 +52,9 @@ struct Kv4Plan {
   size_t ml_bytes, o_bytes, workspace;
 };
 constexpr int kKv4Sms = 148;
-// Rows up to which the decode kernel runs (blocks of 8 or 16 rows). A (b, cached head) of 32 rows over
-// 8 sequences of about 6000 keys and 4 heads: 30.9 us in two blocks of 16, 56.5 in the chunk kernel; of 48 rows 48.9
-// in the chunk kernel and a third block's 15 us more here.
+// Rows of a cached head up to which the decode kernel runs (blocks of 8 or 16 rows; each block reads the
+// keys again, from L2). Both measured: 32 rows over 8 sequences of about 6000 keys x 4 heads 31.9 us here, 41.9 in the
+// chunk kernel; over one sequence of 32768 keys x 8 heads 38.4 and 50.1; 48 rows 46.2 and 48.3; 64 rows 55.9 and 48.7.
 constexpr int kKv4DecodeRows = 32;
 
 Kv4Plan kv4_plan(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {

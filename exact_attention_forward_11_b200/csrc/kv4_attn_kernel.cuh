@@ -20,21 +20,26 @@
 // 16-key group is contiguous in its page: nine 16-byte copies per lane and step, two address
 // computations per group and tensor; bulk copies issued by eight lanes cost more instructions,
 // since each lane's copy is issued in turn) and keeps its own running maximum, sum and O; warps meet
-// only where a segment ends. The
-// maximum moves only when a score exceeds it by more than 8 (log2 units), so most steps cost
-// one vote and no reduction across lanes; P <= 2^8 then, well inside f16.
+// only where a segment ends. The maximum moves only when a score exceeds it by more than 8 (log2
+// units), so most steps cost one vote and no reduction across lanes; P <= 2^8 then, well inside f16.
 //
 // Schedule: the 256-key tiles of all (b, h, row block) make one long list that is cut into
 // equal runs, one per CTA, so uneven lengths balance without the host knowing them. A run
 // that covers part of a (b, h, row block) writes its unnormalised O, maximum and sum to the
 // workspace (two slots per CTA: a run's first and last item); kv4_join_sm100 joins the parts in
 // the order of the runs, so results do not depend on timing. It is launched with programmatic
-// serialisation, so that its launch hides under the main kernel. (A join by the CTA that takes the item's last
-// ticket instead, without a second kernel, was slower: its fence and atomic stand in every split
-// segment's way, 26.6 against 20.8 us on 16 sequences of up to 4096 keys x 8 heads.)
+// serialisation, so that its launch hides under the main kernel. (A join by the CTA that takes
+// the item's last ticket, without a second kernel, was slower: its fence and atomic stand in every split
+// segment's way, 18.4 against 14.4 us on 6 sequences of up to 2047 keys x 12 heads.)
 //
-// Bound: HBM at 4.5 bits a value is 13e12 values / s; a value costs about half a conversion
-// and half a multiplication (64 lanes / clk / SM each).
+// Bound: HBM at 4.5 bits a value is 12e12 values / s, 41 per SM and clock; a value costs half a
+// conversion and half a multiplication (64 lanes / clk / SM each) and with everything else 2.3 / 32 issued
+// instructions. Measured (32 sequences of 32768 keys x 8 heads, d = 128, one token, 4 query heads to a key
+// head): 223 us, 5.4 TB/s of the cache's bytes, 0.83 of the measured copy rate, at 64 % of the issue slots;
+// under a power cap the clock falls and with it the rate (258 us). The list of a run starts after about 7 us
+// (lengths, page numbers, first codes: a chain of three memory latencies) and each further segment costs
+// about 2 us, which is what small batches spend their time on (16 sequences of up to 4096 keys: 24.7 us
+// for 8.1 us of bytes).
 #pragma once
 
 #include "kv4_cache_kernel.cuh"
