@@ -52,6 +52,7 @@ SIGNATURES = {
     "attn_kv4_append": (_I, [_P] * 6 + [_I] * 4 + [_P]),
     "attn_kv4_read": (_I, [_P] * 6 + [_I] * 4 + [_P]),
     "attn_fwd_kv4": (_I, [_P] * 8 + [ctypes.c_size_t] + [_I] * 4 + [_F, _I, _I, _P]),
+    "attn_fwd_kv4_inject_timeout": (_I, [_P] * 8 + [ctypes.c_size_t] + [_I] * 4 + [_F, _I, _I, _I, ctypes.c_ulonglong, _P]),
     "attn_fwd_kv4_workspace_bytes": (ctypes.c_size_t, [_I] * 7),
     "attn_status_string": (ctypes.c_char_p, [_I]),
     "attn_abi_version": (_I, []),
@@ -188,6 +189,14 @@ def attn_fwd_kv4(cache, q, block_table, seq_lens, q_lens, o, lse, workspace, wor
                  scale, causal, dtype, stream):
     return load().attn_fwd_kv4(cache, q, block_table, seq_lens, q_lens, o, lse, workspace, workspace_bytes, B, Hq, N,
                                max_pages, scale, causal, dtype, stream)
+
+
+def attn_fwd_kv4_inject_timeout(cache, q, block_table, seq_lens, q_lens, o, lse, workspace, workspace_bytes, B, Hq, N,
+                                max_pages, scale, causal, dtype, fault_cta, wait_limit_cycles, stream):
+    """Testing hook (include/attn_b200_testing.h): the chunk kernel with one CTA's first key tile withheld."""
+    return load().attn_fwd_kv4_inject_timeout(cache, q, block_table, seq_lens, q_lens, o, lse, workspace, workspace_bytes,
+                                              B, Hq, N, max_pages, scale, causal, dtype, fault_cta, wait_limit_cycles,
+                                              stream)
 
 
 def attn_fwd_kv4_workspace_bytes(B, Hq, Hkv, N, d, page_size, max_pages):

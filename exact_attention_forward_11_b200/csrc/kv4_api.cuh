@@ -16,7 +16,7 @@ attn_status kv4_check_cache(const attn_kv4_cache* c, const int* block_table, con
   if (c->num_pages < 1 || max_pages < 1 || c->page_size < 1) return ATTN_ERR_INVALID_ARG;
   if (c->k_exp < -32 || c->k_exp > 32 || c->v_exp < -32 || c->v_exp > 32) return ATTN_ERR_INVALID_ARG;
   if (c->page_size < 16 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)) != 0) return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(max_pages) * c->page_size >= (1ll << 31)) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_pages) * c->page_size > (1ll << 30)) return ATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(c->num_pages) * c->Hkv >= (1ll << 32) / c->page_size) return ATTN_ERR_INVALID_ARG;
   if (dtype != ATTN_BF16 && dtype != ATTN_FP16) return ATTN_ERR_UNSUPPORTED;
   if (c->d != 64 && c->d != 128) return ATTN_ERR_UNSUPPORTED;
@@ -103,11 +103,11 @@ attn_status launch_kv4_dec(const attn::Kv4AttnParams& p, int tag, cudaStream_t s
 }
 
 template <int D, bool F16, bool PAIR>
-attn_status launch_kv4_chunk(const attn::Kv4AttnParams& p, int tag, cudaStream_t stream) {
+attn_status launch_kv4_chunk(const attn::Kv4AttnParams& p, int tag, cudaStream_t stream, int fault_cta, uint64_t wait_limit) {
   using C = attn::Kv4ChunkCfg<D, PAIR>;
   auto kern = attn::kv4_chunk_sm100<C, F16>;
   if (!set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, tag)) return ATTN_ERR_CUDA;
-  kern<<<p.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(attn::Kv4ChunkParams{p, kWaitLimitCycles});
+  kern<<<p.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(attn::Kv4ChunkParams{p, wait_limit, fault_cta});
   const cudaError_t e = launch_after(attn::kv4_join_sm100<D, attn::kChunkRows, F16>,
                                      dim3(p.ctas, (PAIR ? 128 : attn::kChunkRows) / 8), 256, stream, p);
   if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) {
@@ -118,11 +118,12 @@ attn_status launch_kv4_chunk(const attn::Kv4AttnParams& p, int tag, cudaStream_t
 }
 
 template <int D, bool F16>
-attn_status launch_kv4_rows(const attn::Kv4AttnParams& p, const Kv4Plan& plan, cudaStream_t stream) {
+attn_status launch_kv4_rows(const attn::Kv4AttnParams& p, const Kv4Plan& plan, cudaStream_t stream, int fault_cta,
+                            uint64_t wait_limit) {
   const int tag = 16 + (D == 128 ? 0 : 8) + (F16 ? 4 : 0);
   if (plan.nt == 0)
-    return p.Hq / p.c.H * p.N <= 128 ? launch_kv4_chunk<D, F16, true>(p, tag + 2, stream)
-                                     : launch_kv4_chunk<D, F16, false>(p, tag + 3, stream);
+    return p.Hq / p.c.H * p.N <= 128 ? launch_kv4_chunk<D, F16, true>(p, tag + 2, stream, fault_cta, wait_limit)
+                                     : launch_kv4_chunk<D, F16, false>(p, tag + 3, stream, fault_cta, wait_limit);
   if (plan.nt == 1) return launch_kv4_dec<attn::Kv4DecCfg<D, 1>, F16>(p, tag, stream);
   return launch_kv4_dec<attn::Kv4DecCfg<D, 2>, F16>(p, tag + 1, stream);
 }
@@ -178,9 +179,14 @@ size_t attn_fwd_kv4_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int pa
   return kv4_plan(B, Hq, Hkv, N, d, page_size, max_pages).workspace;
 }
 
-attn_status attn_fwd_kv4(const attn_kv4_cache* cache, const void* q, const int* block_table, const int* seq_lens,
-                         const int* q_lens, void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int Hq,
-                         int N, int max_pages, float scale, int causal, attn_dtype dtype, void* stream) {
+}  // extern "C"
+
+namespace {
+
+attn_status fwd_kv4(const attn_kv4_cache* cache, const void* q, const int* block_table, const int* seq_lens,
+                    const int* q_lens, void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int Hq, int N,
+                    int max_pages, float scale, int causal, attn_dtype dtype, void* stream, int fault_cta,
+                    uint64_t wait_limit) {
   if (q == nullptr || o == nullptr || cache == nullptr) return ATTN_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
   const int d = cache->d, Hkv = cache->Hkv;
@@ -209,8 +215,33 @@ attn_status attn_fwd_kv4(const attn_kv4_cache* cache, const void* q, const int* 
   p.part_o = reinterpret_cast<float*>(ws + plan.ml_bytes);
   p.heads = reinterpret_cast<attn::Kv4Head*>(ws + plan.ml_bytes + plan.o_bytes);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (d == 128) return dtype == ATTN_FP16 ? launch_kv4_rows<128, true>(p, plan, st) : launch_kv4_rows<128, false>(p, plan, st);
-  return dtype == ATTN_FP16 ? launch_kv4_rows<64, true>(p, plan, st) : launch_kv4_rows<64, false>(p, plan, st);
+  const bool f16 = dtype == ATTN_FP16;
+  if (d == 128)
+    return f16 ? launch_kv4_rows<128, true>(p, plan, st, fault_cta, wait_limit)
+               : launch_kv4_rows<128, false>(p, plan, st, fault_cta, wait_limit);
+  return f16 ? launch_kv4_rows<64, true>(p, plan, st, fault_cta, wait_limit)
+             : launch_kv4_rows<64, false>(p, plan, st, fault_cta, wait_limit);
+}
+
+}  // namespace
+
+extern "C" {
+
+attn_status attn_fwd_kv4(const attn_kv4_cache* cache, const void* q, const int* block_table, const int* seq_lens,
+                         const int* q_lens, void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int Hq,
+                         int N, int max_pages, float scale, int causal, attn_dtype dtype, void* stream) {
+  return fwd_kv4(cache, q, block_table, seq_lens, q_lens, o, lse, workspace, workspace_bytes, B, Hq, N, max_pages, scale,
+                 causal, dtype, stream, -1, kWaitLimitCycles);
+}
+
+attn_status attn_fwd_kv4_inject_timeout(const attn_kv4_cache* cache, const void* q, const int* block_table,
+                                        const int* seq_lens, const int* q_lens, void* o, float* lse, void* workspace,
+                                        size_t workspace_bytes, int B, int Hq, int N, int max_pages, float scale,
+                                        int causal, attn_dtype dtype, int fault_cta, unsigned long long wait_limit_cycles,
+                                        void* stream) {
+  if (fault_cta < 0 || wait_limit_cycles < 1024) return ATTN_ERR_INVALID_ARG;
+  return fwd_kv4(cache, q, block_table, seq_lens, q_lens, o, lse, workspace, workspace_bytes, B, Hq, N, max_pages, scale,
+                 causal, dtype, stream, fault_cta, wait_limit_cycles);
 }
 
 }  // extern "C"

@@ -10,7 +10,7 @@
 //    registers (a thread owns one key row), turn them into f16 (one conversion per two codes and one
 //    multiplication by the block scale, both exact) and store them in the 128-byte-swizzled layout
 //    that the MMA reads, K^ and V^ double-buffered. Keys behind the sequence's end are stored as
-//    zeros. (A deeper ring of raw codes in shared memory instead of registers: 1.12 against 1.05 ms, its copies
+//    zeros. (A deeper ring of raw codes in shared memory instead of registers: 1.13 against 1.05 ms, its copies
 //    and loads cost the conversion warps more than the latency they hide.)
 //  * q rows are scaled by a power of two and rounded to f16 by their own softmax threads (the
 //    bf16 q would need bf16 K^; f16 holds every cached value and gives P three more bits).
@@ -92,7 +92,8 @@ struct SfWords { static constexpr int N = D / 64; };   // 32-bit words of a row'
 
 struct Kv4ChunkParams {
   Kv4AttnParams a;           // part_o: [2 ctas][256][D], part_ml: [2 ctas][256]; row_blocks = ceil(R / 256)
-  uint64_t timeout_cycles;
+  uint64_t timeout_cycles;   // per pipeline wait, in SM cycles
+  int fault_cta;             // testing only: this CTA's walk withholds its first key tile (-1: none)
 };
 
 // Key tiles that the 128 rows from r0 of sequence (len, n) see, and (through `all`) the last key
@@ -441,7 +442,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
           for (int i = 0; i < 4; ++i) rows[at * 128 + 32 * i + lane] = rw[i];
           if (lane == 0) edges[at] = w.lim_all - j * 128;
           __syncwarp();
-          if (lane == 0) mbar_arrive(row_full + at);
+          // (testing hook: a tile that is never handed out; the bounded waits on it run out)
+          if (lane == 0 && !(k == 0 && static_cast<int>(blockIdx.x) == cp.fault_cta)) mbar_arrive(row_full + at);
         }
       }
       // the conversion warps stop at the tile that says so

@@ -29,6 +29,7 @@
 #define ATTN_B200_TESTING_H
 
 #include "attn_b200.h"
+#include "kv4_b200.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -81,6 +82,18 @@ ATTN_API attn_status attn_fwd_mxfp8_inject_timeout(const void* q8, const void* k
 ATTN_API attn_status attn_fwd_debug_row_limit(const void* q, const void* k, const void* v, void* o, float* lse,
                                               int B, int H, int N, int d, float scale, int causal,
                                               long long row_limit, void* stream);
+
+/*
+ * attn_fwd_kv4_inject_timeout - attn_fwd_kv4 (kv4_b200.h) with CTA `fault_cta` of the chunk
+ * kernel never handing out its first key tile and every wait limited to wait_limit_cycles:
+ * the CTA's waits run out and the launch reports ATTN_ERR_TIMEOUT; what other CTAs alone
+ * compute is exact. Calls of few rows run the decode kernel, which waits on nothing: unaffected.
+ */
+ATTN_API attn_status attn_fwd_kv4_inject_timeout(const attn_kv4_cache* cache, const void* q, const int* block_table,
+                                                 const int* seq_lens, const int* q_lens, void* o, float* lse,
+                                                 void* workspace, size_t workspace_bytes, int B, int Hq, int N,
+                                                 int max_pages, float scale, int causal, attn_dtype dtype, int fault_cta,
+                                                 unsigned long long wait_limit_cycles, void* stream);
 
 #ifdef __cplusplus
 }

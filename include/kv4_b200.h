@@ -27,7 +27,7 @@
  *   block_table      : [B, max_pages] int32; position p of sequence b lies in page
  *                      block_table[b, p / page_size], slot p % page_size.
  *   seq_lens         : [B] int32 tokens of each sequence in the cache, 0 or more.
- * page_size is a power of two from 16 to 65536 (else ATTN_ERR_UNSUPPORTED); max_pages * page_size < 2^31;
+ * page_size is a power of two from 16 to 65536 (else ATTN_ERR_UNSUPPORTED); max_pages * page_size <= 2^30;
  * num_pages * Hkv * page_size < 2^32; d is 64 or 128 (else ATTN_ERR_UNSUPPORTED);
  * |k_exp|, |v_exp| <= 32. dtype (of k, v, q, o) is ATTN_BF16 or ATTN_FP16.
  *
@@ -94,7 +94,8 @@ ATTN_API attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block
  *   q_lens : [B] int32, 0 <= q_lens[b] <= N, or NULL for N. Query i < q_lens[b] is the
  *          token at position seq_lens[b] - q_lens[b] + i; it sees the keys at positions
  *          j < seq_lens[b], and with causal = 1 only j <= its own.
- *   o    : [B, Hq, N, d] output softmax(scale q K^T) V over the values as read back.
+ *   o    : [B, Hq, N, d] output softmax(scale q K^T) V over the values as read back
+ *          (must not alias q).
  *   lse  : [B, Hq, N] fp32 (natural log, scale included), or NULL.
  *          Rows i >= q_lens[b] of o and lse are left as they were. A row that sees no
  *          key gets o = 0 and lse = -infinity. A row that sees a NaN key or value is

@@ -35,7 +35,7 @@ SHARED = [(dict(cache=None), 1), (dict(k_codes=None), 1), (dict(v_sf=None), 1), 
           (dict(B=0), 1), (dict(Hkv=0), 1), (dict(N=-1), 1), (dict(num_pages=0), 1), (dict(maxp=0), 1),
           (dict(page_size=0), 1), (dict(page_size=24), 2), (dict(page_size=8), 2), (dict(page_size=1 << 17), 2),
           (dict(d=96), 2), (dict(d=256), 2), (dict(dtype=2), 2), (dict(k_exp=33), 1), (dict(v_exp=-33), 1),
-          (dict(page_size=65536, maxp=1 << 15), 1), (dict(num_pages=1 << 30), 1), (dict(B=1 << 16, N=1 << 15), 1),
+          (dict(page_size=65536, maxp=(1 << 14) + 1), 1), (dict(num_pages=1 << 30), 1), (dict(B=1 << 16, N=1 << 15), 1),
           (dict(k_codes=FAKE + 2), 3), (dict(v_sf=FAKE + 8), 3), (dict(bt=FAKE + 2), 3), (dict(sl=FAKE + 1), 3)]
 
 
@@ -55,6 +55,14 @@ def test_append_and_read_refuse(lib, change, status):
 def test_forward_refuses(lib, change, status):
     addr, a = split(FWD, change)
     assert lib.attn_fwd_kv4(addr, *a.values()) == status
+
+
+def test_timeout_hook_refuses(lib):
+    addr, a = split(FWD, {})
+    *rest, stream = a.values()
+    assert lib.attn_fwd_kv4_inject_timeout(addr, *rest, -1, 1 << 22, stream) == 1
+    assert lib.attn_fwd_kv4_inject_timeout(addr, *rest, 0, 100, stream) == 1
+    assert lib.attn_fwd_kv4_inject_timeout(None, *rest, 0, 1 << 22, stream) == 1
 
 
 def test_workspace_bytes_and_a_small_workspace(lib):
