@@ -49,6 +49,7 @@ attn::Kv4Cache kv4_cache_of(const attn_kv4_cache* from, const int* block_table, 
 struct Kv4Plan {
   int nt;                    // decode kernel: 8-row tiles per block; 0: the chunk kernel
   int row_blocks, ctas;
+  bool fits;                 // the decode kernel's units (see Kv4Runs) stay below 2^31
   size_t ml_bytes, o_bytes, workspace;
 };
 constexpr int kKv4Sms = 148;
@@ -67,6 +68,7 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pa
   const long long most = kKv4Sms * (r.nt == 1 ? 2 : 1);
   const double units = static_cast<double>(tiles) * B * Hkv * r.row_blocks;
   r.ctas = static_cast<int>(units < most ? units : most);
+  r.fits = r.nt == 0 || units + static_cast<double>(attn::kDecSegmentTiles) * B * Hkv * r.row_blocks < 2147483648.0;
   r.ml_bytes = static_cast<size_t>(2) * r.ctas * block * sizeof(float2);
   r.o_bytes = static_cast<size_t>(2) * r.ctas * block * d * sizeof(float);
   r.workspace = r.ml_bytes + r.o_bytes + (r.ctas * sizeof(attn::Kv4Head) + 15) / 16 * 16;
@@ -176,7 +178,8 @@ attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block_table, c
 size_t attn_fwd_kv4_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {
   if (B < 1 || Hq < 1 || Hkv < 1 || N < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
   if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0 || max_pages < 1) return 0;
-  return kv4_plan(B, Hq, Hkv, N, d, page_size, max_pages).workspace;
+  const Kv4Plan plan = kv4_plan(B, Hq, Hkv, N, d, page_size, max_pages);
+  return plan.fits ? plan.workspace : 0;
 }
 
 }  // extern "C"
@@ -195,7 +198,7 @@ attn_status fwd_kv4(const attn_kv4_cache* cache, const void* q, const int* block
   if (attn_status s = check_shape(B, Hq, N); s != ATTN_OK) return s;
   if (attn_status s = kv4_check_cache(cache, block_table, seq_lens, B, N, max_pages, dtype); s != ATTN_OK) return s;
   const Kv4Plan plan = kv4_plan(B, Hq, Hkv, N, d, cache->page_size, max_pages);
-  if (workspace == nullptr || workspace_bytes < plan.workspace) return ATTN_ERR_INVALID_ARG;
+  if (!plan.fits || workspace == nullptr || workspace_bytes < plan.workspace) return ATTN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned4(q_lens) || !aligned16(workspace))
     return ATTN_ERR_MISALIGNED;
   attn::Kv4AttnParams p{};

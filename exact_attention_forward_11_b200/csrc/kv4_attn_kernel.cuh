@@ -49,6 +49,7 @@ namespace attn {
 constexpr int kDecWarps = 8;
 constexpr int kDecKeys = 32;                       // keys of a warp's step
 constexpr int kDecTile = kDecWarps * kDecKeys;     // 256
+constexpr int kDecSegmentTiles = 2, kDecJoinTiles = 2;   // what the cut counts with: see Kv4Runs
 
 template <int D_, int NT_>
 struct Kv4DecCfg {
@@ -99,18 +100,56 @@ __device__ __forceinline__ int kv4_tiles(const Kv4AttnParams& p, int b) {
   return kv4_qlen(p, b) == 0 ? 0 : (kv4_len(p.c, b) + kDecTile - 1) / kDecTile;
 }
 
-// The cut of `units` tiles into runs: CTA c of n = min(ctas, units) takes [start(c), start(c + 1)).
+// The cut of the tiles into runs, one a CTA. A further item of a run costs its CTA about kDecSegmentTiles tiles (the
+// pipeline drains, results meet, q is read), and items that are cut cost the join about kDecJoinTiles.
+//   * Whole items, k a CTA, if their longest run is no longer than an even cut's with the join: an item counts as
+//     `whole` tiles whatever its length.
+//   * Else an even cut, in which an item counts as lead + T tiles, its first `lead` without work, where runs are long
+//     enough for it to matter (four tiles each; below, lead = 0).
+// Measured (d = 128, 32 query heads on 8, one query): 64 sequences of 1000 keys 29.6 us in whole items, 32.2 in an even
+// cut; 8 of 700 keys 9.3 and 10.7; 8 of 1000 keys (an even cut) 11.4, whole 10.9, but 32 of 1000 keys x 1 head 9.8 and
+// 10.9; 12 of 4096 keys (an even cut) 23.1 with the leads, 24.8 without; one of 4096 keys 14.0 without, 15.2 with them.
+// CTA c of n takes the units [start(c), start(c + 1)). (Host: fewer than 2^31.)
 struct Kv4Runs {
-  long long units;
-  int n;
-  __device__ __forceinline__ Kv4Runs(long long u, int ctas) : units(u), n(static_cast<int>(u < ctas ? u : ctas)) {}
-  __device__ __forceinline__ long long start(int c) const { return units * c / n; }
-  __device__ __forceinline__ int cta_of(long long u) const { return static_cast<int>(((u + 1) * n - 1) / units); }
+  uint32_t units, base, rem;
+  int n, lead, whole;
+  __device__ __forceinline__ Kv4Runs(uint32_t tiles, uint32_t items, uint32_t longest, uint32_t ctas) {
+    const uint32_t even = (tiles + items * kDecSegmentTiles) / ctas, k = (items + ctas - 1) / ctas;
+    if (k * (longest + kDecSegmentTiles) <= even + kDecSegmentTiles + kDecJoinTiles) {
+      lead = 0;
+      whole = static_cast<int>(longest);
+      units = items * longest;
+      n = k > 0 ? static_cast<int>((items + k - 1) / k) : 0;
+      base = k * longest;
+      rem = 0;
+    } else {
+      lead = tiles >= 4 * ctas ? kDecSegmentTiles : 0;
+      whole = 0;
+      units = tiles + items * static_cast<uint32_t>(lead);
+      n = static_cast<int>(min(units, ctas));
+      base = units / static_cast<uint32_t>(n);
+      rem = units - base * static_cast<uint32_t>(n);
+    }
+  }
+  __device__ __forceinline__ uint32_t start(int c) const {
+    return min(base * c + min(static_cast<uint32_t>(c), rem), units);
+  }
+  __device__ __forceinline__ int cta_of(uint32_t u) const {
+    const uint32_t longer = rem * (base + 1u);
+    return static_cast<int>(u < longer ? u / (base + 1u) : rem + (u - longer) / base);
+  }
+  __device__ __forceinline__ uint32_t item_units(int T) const {   // of an item of T > 0 tiles
+    return static_cast<uint32_t>(max(T + lead, whole));
+  }
 };
 
-__device__ __forceinline__ long long warp_sum(long long v) {
+__device__ __forceinline__ uint32_t warp_sum(uint32_t v) { return __reduce_add_sync(0xffffffffu, v); }
+__device__ __forceinline__ uint32_t warp_prefix(uint32_t v, int lane) {     // inclusive
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  for (int s = 1; s < 32; s <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, v, s);
+    if (lane >= s) v += o;
+  }
   return v;
 }
 
@@ -218,32 +257,30 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
   // stay in the lanes; more are read again.
   const int per_b = p.c.H * p.row_blocks;
   const bool few = p.c.B <= 32;
-  int my_len = 0, my_n = 0;                         // of sequence `lane`, if few
-  long long total = 0;
+  int my_len = 0, my_n = 0, my_T = 0;                         // of sequence `lane`, if few
+  uint32_t tiles = 0, items = 0, longest = 0;
   bool blind = false;                               // some row sees no key
   for (int i = lane; i < p.c.B; i += 32) {
     my_len = kv4_len(p.c, i);
     my_n = kv4_qlen(p, i);
-    total += my_n == 0 ? 0 : (my_len + kDecTile - 1) / kDecTile;
+    const uint32_t T = my_n == 0 ? 0u : static_cast<uint32_t>(my_len + kDecTile - 1) / kDecTile;
+    tiles += T * per_b;
+    items += T > 0u ? per_b : 0u;
+    longest = max(longest, T);
+    my_T = static_cast<int>(T);
     blind = blind || (my_n > 0 && (my_len == 0 || (p.causal && my_n > my_len)));
   }
   if (__any_sync(0xffffffffu, blind)) kv4_empty_rows<D>(p, tid, kDecWarps * 32);
-  const long long my_units = total * per_b;
-  const Kv4Runs runs(warp_sum(my_units), p.ctas);
+  const Kv4Runs runs(warp_sum(tiles), warp_sum(items), __reduce_max_sync(0xffffffffu, longest), p.ctas);
   if (static_cast<int>(blockIdx.x) >= runs.n) return;
-  long long u = runs.start(blockIdx.x);
-  const long long u_begin = u, u_end = runs.start(blockIdx.x + 1);
+  uint32_t u = runs.start(blockIdx.x);
+  const uint32_t u_end = runs.start(blockIdx.x + 1);
+  auto units_of = [&](int T) { return T > 0 ? runs.item_units(T) * per_b : 0u; };
   int b = 0;
-  long long b_first = 0;                            // first unit of sequence b
+  uint32_t b_first = 0;                             // first unit of sequence b
   for (int b0 = 0;; b0 += 32) {
-    const long long mine =
-        few ? my_units : (b0 + lane < p.c.B ? static_cast<long long>(kv4_tiles(p, b0 + lane)) * per_b : 0);
-    long long incl = mine;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, incl, s);
-      if (lane >= s) incl += o;
-    }
+    const uint32_t mine = b0 + lane < p.c.B ? units_of(few ? my_T : kv4_tiles(p, b0 + lane)) : 0u;
+    const uint32_t incl = warp_prefix(mine, lane);
     const uint32_t hit = __ballot_sync(0xffffffffu, b_first + incl > u);
     if (hit != 0u) {
       const int l = __ffs(hit) - 1;
@@ -259,28 +296,34 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
   // the segment being worked on: tiles [t0, t1) of T of (b, h, row block rb)
   int T, h, rb, t0, t1, len, n, steps_end, base0;
   uint32_t hrow;
-  long long item_first;
+  uint32_t item_first;                              // its item's first tile, as a unit
   size_t row0;                                      // rows of (b, h) are contiguous in q and o
   const int* table;
-  auto find_segment = [&]() {                       // the one that starts at unit u
-    for (;;) {
+  auto find_segment = [&]() {                       // the first with work at or after unit u; moves u behind it
+    while (u < u_end) {
       len = few ? __shfl_sync(0xffffffffu, my_len, b) : kv4_len(p.c, b);
       n = few ? __shfl_sync(0xffffffffu, my_n, b) : kv4_qlen(p, b);
       T = n == 0 ? 0 : (len + kDecTile - 1) / kDecTile;
-      if (u < b_first + static_cast<long long>(T) * per_b) break;
-      b_first += static_cast<long long>(T) * per_b;  // (sequences without tiles are passed over)
-      ++b;
+      if (u >= b_first + units_of(T)) {
+        b_first += units_of(T);
+        ++b;
+        continue;
+      }
+      const uint32_t per = runs.item_units(T), item = (u - b_first) / per;
+      item_first = b_first + (item + 1u) * per - static_cast<uint32_t>(T);
+      h = static_cast<int>(item) / p.row_blocks, rb = static_cast<int>(item) % p.row_blocks;
+      t0 = max(0, static_cast<int>(u - item_first));
+      t1 = min(T, static_cast<int>(u_end - item_first));
+      u = item_first + max(t1, 0);
+      if (t1 <= t0) return false;                   // the run ends before the item's first tile
+      row0 = (static_cast<size_t>(b) * p.c.H + h) * R;
+      table = p.c.block_table + static_cast<long long>(b) * p.c.max_pages;
+      steps_end = min(t1 * kDecTile, len);          // its keys end here
+      base0 = t0 * kDecTile + warp * kDecKeys;      // this warp's first step
+      hrow = static_cast<uint32_t>(h) << p.c.page_shift;
+      return true;
     }
-    const int item = static_cast<int>(static_cast<uint32_t>(u - b_first) / static_cast<uint32_t>(T));
-    item_first = b_first + static_cast<long long>(item) * T;
-    h = item / p.row_blocks, rb = item % p.row_blocks;
-    t0 = static_cast<int>(u - item_first);
-    t1 = static_cast<int>(min(static_cast<long long>(T), u_end - item_first));
-    row0 = (static_cast<size_t>(b) * p.c.H + h) * R;
-    table = p.c.block_table + static_cast<long long>(b) * p.c.max_pages;
-    steps_end = min(t1 * kDecTile, len);            // its keys end here
-    base0 = t0 * kDecTile + warp * kDecKeys;        // this warp's first step
-    hrow = static_cast<uint32_t>(h) << p.c.page_shift;
+    return false;
   };
 
   // ---- a warp's pipeline over its 32-key steps
@@ -358,7 +401,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
     }
   };
 
-  find_segment();
+  if (!find_segment()) return;
+  bool first_segment = true;
   start_segment(C::STAGES - 1);
   if (AHEAD) load_q(0);
   for (;;) {
@@ -587,7 +631,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
     if (base0 + (t1 - t0 - 1) * kDecTile >= steps_end) rd = after(rd);   // the last tile ends before this warp's
                                                     // keys: every warp's ring stands at the same stage
     const bool whole = t0 == 0 && t1 == T;
-    const int slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
+    const int slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
+    first_segment = false;
     const int out_rb = rb, out_n = n;
     if (tid == 0 && t0 == 0 && !whole) {            // the item's first part: what the join needs
       Kv4Head hd;
@@ -596,11 +641,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
       p.heads[blockIdx.x] = hd;
     }
     const size_t out_row0 = row0;
-    u = item_first + t1;
     wr = rd;
-    const bool more = u < u_end;
+    const bool more = find_segment();
     if (more) {
-      find_segment();
       start_segment(C::STAGES - NT);
     } else {
       for (int i = 0; i < C::STAGES - NT; ++i) wr = after(wr);

@@ -116,3 +116,12 @@ def test_binding_refuses_tensors_gpu(cuda_lib):
         lib.kv4_append(lib.KV4Cache(c.k_codes, c.k_sf, c.v_codes, c.v_sf, k_exp=40), k, k, bt, sl)
     torch.cuda.synchronize()
     assert lib.attn_get_device_status(None) == lib.ATTN_OK
+
+
+def test_too_many_tiles_are_refused(lib):
+    wsb = lib.attn_fwd_kv4_workspace_bytes
+    tiles = (1 << 30) // 256                                   # of the longest table
+    assert wsb(1, 511, 511, 1, 128, 65536, 1 << 14) > 0        # 511 (tiles + 2) < 2^31
+    assert wsb(1, 512, 512, 1, 128, 65536, 1 << 14) == 0 and 512 * tiles == 1 << 31
+    addr, a = split(FWD, dict(page_size=65536, maxp=1 << 14, num_pages=1, Hkv=512, Hq=512, N=1))
+    assert lib.attn_fwd_kv4(addr, *a.values()) == 1

@@ -571,3 +571,19 @@ def test_chunk_kernel_timeout_path(cuda_lib, N, Hq):
         o.zero_(), lse.zero_()
     again = lib.forward_kv4(q, pg.cache, pg.bt, ints(lens), check=True)
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+@pytest.mark.parametrize("N,lens,H", [
+    (1, [5000, 0, 4097, 257, 7000, 3000], 16),                      # runs of 4 to 5 tiles, items of 2 to 28
+    (2, [5000, 0, 4097, 257, 7000, 3000], 16),                      # the same in blocks of 16 rows (q heads 6 a head)
+    (1, [256 * (b % 4) + b for b in range(40)], 24),                # more sequences than lanes, items of 0 to 4 tiles
+    (1, [(37 * b) % 512 for b in range(70)], 8),                    # whole items, two a CTA, the last CTA's one
+    (5, [(53 * b) % 700 for b in range(31)], 3)])                   # whole items of 0 to 3 tiles, two blocks of rows
+def test_long_runs(cuda_lib, N, lens, H):
+    """Runs of several items: segments that start and end anywhere in an item, and runs of whole items."""
+    lib, B, d = cuda_lib, len(lens), 64
+    pg = Paged(lib, B, H, d, 64, (max(lens) + 63) // 64, seed=B)
+    fill(pg, lens, torch.bfloat16, 9)
+    q = make_q(B, 6 * H, N, d, torch.bfloat16, 8)
+    o, lse = lib.forward_kv4(q, pg.cache, pg.bt, ints(lens), causal=True, check=True)
+    check_attention(o, lse, q, pg, lens, [N] * B, True)
