@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 RELEASE_LIB_PATH = os.path.join(_HERE, "libattn_b200.so")
@@ -723,19 +724,21 @@ def kv4_read(cache, block_table, seq_lens, N, starts=None, dtype=None, k=None, v
     return k, v
 
 
-# workspaces of forward_kv4, one per (device, stream): launches of one stream run in order
-_KV4_WORKSPACES = {}
+# workspaces of forward_kv4, one per (device, stream) of each host thread: launches of one stream run in order, but
+# a call is two launches, between which another thread's may come
+_KV4_WORKSPACES = threading.local()
 
 
 def _kv4_workspace(cache, sp, need):
     if torch._C._cuda_isCurrentStreamCapturing():
         # a graph has its own: it may be replayed on any stream, next to any other call
         return torch.empty(need, dtype=torch.uint8, device=cache.device)
+    kept = _KV4_WORKSPACES.__dict__
     key = (cache._index, sp)
-    ws = _KV4_WORKSPACES.get(key)
+    ws = kept.get(key)
     if ws is None or ws.shape[0] < need:
         # (made with that stream current: the memory of the old one goes back to its pool)
-        ws = _KV4_WORKSPACES[key] = torch.empty(need, dtype=torch.uint8, device=cache.device)
+        ws = kept[key] = torch.empty(need, dtype=torch.uint8, device=cache.device)
     return ws
 
 
@@ -750,7 +753,7 @@ def forward_kv4(q, cache, block_table, seq_lens, q_lens=None, causal=False, scal
     own. N = 1 is a decoding step. Rows behind q_lens[b] are left as they were in out
     and lse (zero where those are allocated here); a row that sees no key gets O = 0,
     LSE = -inf. `workspace`: a uint8 tensor of at least attn_fwd_kv4_workspace_bytes(...);
-    None: one kept per device and stream (inside a graph capture: the graph's own).
+    None: one kept per thread, device and stream (inside a graph capture: the graph's own).
     Asynchronous like forward(); bad page numbers and lengths as in kv4_append."""
     B, Hq, N, dt = _kv4_rows(q, "q", cache)
     bt, max_pages = _kv4_table(block_table, B, cache)

@@ -101,8 +101,9 @@ ATTN_API attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block
  *          key gets o = 0 and lse = -infinity. A row that sees a NaN key or value is
  *          NaN; rows that do not see it are unaffected.
  *   workspace : at least attn_fwd_kv4_workspace_bytes(...) bytes, 16-byte aligned,
- *          overwritten; needs no initialisation. Calls that overlap on the GPU need
- *          separate workspaces.
+ *          overwritten; needs no initialisation. Calls that overlap on the GPU, or that
+ *          two host threads make at the same time, on one stream even (a call is two
+ *          launches), need separate workspaces.
  *   scale: 0 selects 1/sqrt(d).
  *   Size: with R = Hq / Hkv * N <= 32 rows of a cached head, at most 2^31 tiles of 256
  *          keys: B * Hkv * ceil(R / 8) * (ceil(max_pages * page_size / 256) + 2) < 2^31 (R <= 8;

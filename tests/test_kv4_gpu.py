@@ -18,6 +18,7 @@ with ds' = ds + 2^-22 max|S|.
 """
 import math
 import os
+import threading
 
 import numpy as np
 import pytest
@@ -587,3 +588,37 @@ def test_long_runs(cuda_lib, N, lens, H):
     q = make_q(B, 6 * H, N, d, torch.bfloat16, 8)
     o, lse = lib.forward_kv4(q, pg.cache, pg.bt, ints(lens), causal=True, check=True)
     check_attention(o, lse, q, pg, lens, [N] * B, True)
+
+
+def test_threads_on_one_stream(cuda_lib):
+    """Two host threads that call on one stream: each has its own workspace, since their launches may interleave."""
+    lib, d = cuda_lib, 128
+    torch.cuda.synchronize()
+    pgs, qs, want = [], [], []
+    for t, (B, N, lens) in enumerate([(3, 1, [1500, 40, 2100]), (2, 40, [700, 1300])]):
+        pg = Paged(lib, B, 2, d, 16, (max(lens) + 15) // 16, seed=t)
+        fill(pg, lens, torch.bfloat16, t)
+        pgs.append((pg, ints(lens)))
+        qs.append(make_q(B, 8, N, d, torch.bfloat16, t))
+        want.append(lib.forward_kv4(qs[t], pg.cache, pg.bt, pgs[t][1], causal=True, check=True))
+    got, places, both = [[], []], [None, None], threading.Barrier(2)
+
+    def work(t):
+        pg, lens = pgs[t]
+        both.wait(60)
+        for _ in range(200):
+            got[t].append(lib.forward_kv4(qs[t], pg.cache, pg.bt, lens, causal=True))
+        places[t] = lib._kv4_workspace(pg.cache, torch.cuda.current_stream().cuda_stream, 16).data_ptr()
+        both.wait(60)                                              # (a thread's workspace is freed with it)
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert None not in places and places[0] != places[1]
+    for t in range(2):
+        assert len(got[t]) == 200
+        for o, lse in got[t]:
+            assert torch.equal(o, want[t][0]) and torch.equal(lse, want[t][1])
