@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 import threading
 
@@ -571,8 +572,8 @@ def w4a16_matmul(x, qweight, scales, zeros, out=None, stream=None, check=False, 
 class KV4Cache:
     """The tensors of a 4-bit key/value cache (format: include/kv4_b200.h) and their
     exponents: k_codes, v_codes uint8 [num_pages, Hkv, page_size, d / 2], k_sf, v_sf uint8
-    [num_pages, Hkv, page_size, d / 16]. The handle checks them once and keeps them;
-    KV4Cache.allocate makes new ones. A value reads back as code * scale * 2^exp:
+    [num_pages, Hkv, page_size, d / 16]. The handle checks them once and keeps them (its
+    attributes cannot be set); KV4Cache.allocate makes new ones. A value reads back as code * scale * 2^exp:
     exponents other than 0 suit tensors whose values are mostly below about 0.1 or
     above 2000."""
 
@@ -590,14 +591,17 @@ class KV4Cache:
         for name, t, width in (("k_codes", k_codes, half), ("v_codes", v_codes, half), ("k_sf", k_sf, half // 8),
                                ("v_sf", v_sf, half // 8)):
             _expect(t, name, (P, H, S, width), torch.uint8, k_codes.device)
-        self.k_codes, self.k_sf, self.v_codes, self.v_sf = k_codes, k_sf, v_codes, v_sf
-        self.k_exp, self.v_exp = int(k_exp), int(v_exp)
-        self.num_pages, self.heads, self.page_size, self.d, self.device = P, H, S, 2 * half, k_codes.device
-        self._index = k_codes.get_device()
-        self._struct = attn_kv4_cache(*(t.data_ptr() for t in (k_codes, k_sf, v_codes, v_sf)), P, S, H, 2 * half,
-                                      self.k_exp, self.v_exp)
-        self._addr = ctypes.addressof(self._struct)
-        self._need = {}      # workspace bytes of forward_kv4 by (B, Hq, N, max_pages)
+        struct = attn_kv4_cache(*(t.data_ptr() for t in (k_codes, k_sf, v_codes, v_sf)), P, S, H, 2 * half,
+                                operator.index(k_exp), operator.index(v_exp))
+        for name, value in dict(k_codes=k_codes, k_sf=k_sf, v_codes=v_codes, v_sf=v_sf, k_exp=struct.k_exp,
+                                v_exp=struct.v_exp, num_pages=P, heads=H, page_size=S, d=2 * half,
+                                device=k_codes.device, _index=k_codes.get_device(), _struct=struct,
+                                _addr=ctypes.addressof(struct),
+                                _need={}).items():     # _need: workspace bytes of forward_kv4 by (B, Hq, N, max_pages)
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a KV4Cache is fixed: make another handle")
 
     @classmethod
     def allocate(cls, num_pages, heads, page_size, d, k_exp=0, v_exp=0, device="cuda"):
@@ -650,6 +654,8 @@ class _kv4_place:
     def __init__(self, device, stream):
         self.ctx = [torch.cuda.device(device)]
         if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream must be a stream of {device}")
             self.ctx.append(torch.cuda.stream(stream))
         for c in self.ctx:
             c.__enter__()

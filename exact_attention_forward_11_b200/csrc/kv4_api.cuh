@@ -190,7 +190,7 @@ attn_status fwd_kv4(const attn_kv4_cache* cache, const void* q, const int* block
                     const int* q_lens, void* o, float* lse, void* workspace, size_t workspace_bytes, int B, int Hq, int N,
                     int max_pages, float scale, int causal, attn_dtype dtype, void* stream, int fault_cta,
                     uint64_t wait_limit) {
-  if (q == nullptr || o == nullptr || cache == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (q == nullptr || o == nullptr || q == o || cache == nullptr) return ATTN_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
   const int d = cache->d, Hkv = cache->Hkv;
   if (attn_status s = resolve_scale(scale, d > 0 ? d : 1); s != ATTN_OK) return s;

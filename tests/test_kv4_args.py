@@ -18,7 +18,7 @@ def lib():
 
 CACHE = dict(k_codes=FAKE, k_sf=FAKE, v_codes=FAKE, v_sf=FAKE, num_pages=4, page_size=16, Hkv=2, d=128, k_exp=0, v_exp=0)
 MOVE = dict(k=FAKE, v=FAKE, bt=FAKE, sl=FAKE, first=None, B=1, N=3, maxp=2, dtype=0, stream=None)
-FWD = dict(q=FAKE, bt=FAKE, sl=FAKE, ql=None, o=FAKE, lse=None, ws=FAKE, wsb=1 << 40, B=1, Hq=4, N=3, maxp=2, scale=0.0,
+FWD = dict(q=FAKE, bt=FAKE, sl=FAKE, ql=None, o=2 * FAKE, lse=None, ws=FAKE, wsb=1 << 40, B=1, Hq=4, N=3, maxp=2, scale=0.0,
            causal=0, dtype=0, stream=None)
 
 
@@ -49,7 +49,7 @@ def test_append_and_read_refuse(lib, change, status):
 
 
 @pytest.mark.parametrize("change,status", SHARED + [
-    (dict(q=None), 1), (dict(o=None), 1), (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(causal=2), 1), (dict(scale=-1.0), 1),
+    (dict(q=None), 1), (dict(o=None), 1), (dict(o=FAKE), 1), (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(causal=2), 1), (dict(scale=-1.0), 1),
     (dict(scale=float("nan")), 1), (dict(q=FAKE + 4), 3), (dict(lse=FAKE + 4), 3), (dict(ql=FAKE + 1), 3),
     (dict(ws=FAKE + 8), 3)])
 def test_forward_refuses(lib, change, status):
@@ -125,3 +125,24 @@ def test_too_many_tiles_are_refused(lib):
     assert wsb(1, 512, 512, 1, 128, 65536, 1 << 14) == 0 and 512 * tiles == 1 << 31
     addr, a = split(FWD, dict(page_size=65536, maxp=1 << 14, num_pages=1, Hkv=512, Hq=512, N=1))
     assert lib.attn_fwd_kv4(addr, *a.values()) == 1
+
+
+@pytest.mark.gpu
+def test_handle_is_fixed_and_streams_of_another_device_are_refused(cuda_lib):
+    lib, dev = cuda_lib, torch.device("cuda:0")
+    c = lib.KV4Cache.allocate(4, 2, 16, 128, k_exp=-1)
+    for name, value in (("k_exp", 2), ("v_codes", c.k_codes), ("heads", 1)):
+        with pytest.raises(AttributeError):
+            setattr(c, name, value)
+    assert c.k_exp == -1 and c.heads == 2
+    with pytest.raises(TypeError):
+        lib.KV4Cache(c.k_codes, c.k_sf, c.v_codes, c.v_sf, k_exp=0.5)
+
+    class Elsewhere:                                           # stands for a stream of a second GPU
+        device = torch.device("cuda:1")
+        cuda_stream = 0
+
+    bt, sl = torch.zeros(2, 3, dtype=torch.int32, device=dev), torch.ones(2, dtype=torch.int32, device=dev)
+    with pytest.raises(ValueError):
+        lib.kv4_read(c, bt, sl, 4, stream=Elsewhere())
+    torch.cuda.synchronize()
