@@ -613,36 +613,35 @@ class KV4Cache:
 
 
 def _kv4_int32(t, name, shape, cache):
-    if t.dtype is not torch.int32 or t.get_device() != cache._index or t.shape != shape or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not torch.int32 or t.get_device() != cache._index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {cache.device}")
     return t.data_ptr()
 
 
 def _kv4_rows(t, name, cache):
-    """Sizes and element type of a 16-bit [B, H, N, d] argument of the cache calls."""
-    dt = t.dtype
-    shape = t.shape
+    """Shape, element type and its code of a 16-bit [B, H, N, d] argument of the cache calls."""
+    dtype, shape = t.dtype, t.shape
+    dt = ATTN_BF16 if dtype is torch.bfloat16 else ATTN_FP16
     if len(shape) != 4 or t.get_device() != cache._index or not t.is_contiguous() or \
-            (dt is not torch.bfloat16 and dt is not torch.float16):
+            (dt == ATTN_FP16 and dtype is not torch.float16):
         raise ValueError(f"{name} must be a contiguous bf16 or fp16 tensor [B, H, N, d] on {cache.device}")
-    B, H, N, d = shape
-    if d != cache.d:
-        raise ValueError(f"{name} has heads of width {d}: the cache has {cache.d}")
-    return B, H, N, ATTN_BF16 if dt is torch.bfloat16 else ATTN_FP16
+    if shape[3] != cache.d:
+        raise ValueError(f"{name} has heads of width {shape[3]}: the cache has {cache.d}")
+    return shape, dtype, dt
 
 
-def _kv4_like(t, name, ref):
-    """A tensor argument that must be like `ref`."""
-    if t.shape != ref.shape or t.dtype is not ref.dtype or t.get_device() != ref.get_device() or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {ref.dtype} tensor of shape {tuple(ref.shape)} on {ref.device}")
+def _kv4_like(t, name, shape, dtype, cache):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != cache._index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {cache.device}")
     return t.data_ptr()
 
 
 def _kv4_table(t, B, cache):
     shape = t.shape
-    if len(shape) != 2 or shape[0] != B:
-        raise ValueError(f"block_table must be int32 [{B}, max_pages]")
-    return _kv4_int32(t, "block_table", shape, cache), shape[1]
+    if len(shape) != 2 or shape[0] != B or t.dtype is not torch.int32 or t.get_device() != cache._index or \
+            not t.is_contiguous():
+        raise ValueError(f"block_table must be a contiguous int32 tensor [{B}, max_pages] on {cache.device}")
+    return t.data_ptr(), shape[1]
 
 
 class _kv4_place:
@@ -684,15 +683,17 @@ def kv4_append(cache, k, v, block_table, seq_lens, new_lens=None, stream=None, c
     block_table[b, position // page_size]. Asynchronous; a page number or length outside
     the cache skips the write and is reported by attn_get_device_status()
     (check=True waits and raises). Returns the cache."""
-    B, H, N, dt = _kv4_rows(k, "k", cache)
+    shape, dtype, dt = _kv4_rows(k, "k", cache)
+    B, H, N, _ = shape
     if H != cache.heads:
         raise ValueError(f"k has {H} heads: the cache has {cache.heads}")
+    vp = _kv4_like(v, "v", shape, dtype, cache)
     bt, max_pages = _kv4_table(block_table, B, cache)
-    args = (cache._addr, k.data_ptr(), _kv4_like(v, "v", k), bt, _kv4_int32(seq_lens, "seq_lens", (B,), cache),
-            None if new_lens is None else _kv4_int32(new_lens, "new_lens", (B,), cache), B, N, max_pages, dt)
+    sl = _kv4_int32(seq_lens, "seq_lens", (B,), cache)
+    nl = None if new_lens is None else _kv4_int32(new_lens, "new_lens", (B,), cache)
     sp, place = _kv4_stream(cache, stream)
     try:
-        st = load().attn_kv4_append(*args, sp)
+        st = load().attn_kv4_append(cache._addr, k.data_ptr(), vp, bt, sl, nl, B, N, max_pages, dt, sp)
         if st or check:
             _check(st, "attn_kv4_append")
             _check_device(check, sp, "attn_kv4_append")
@@ -713,14 +714,17 @@ def kv4_read(cache, block_table, seq_lens, N, starts=None, dtype=None, k=None, v
     sp, place = _kv4_stream(cache, stream)
     try:
         if k is None:
-            k = torch.empty((B, cache.heads, N, cache.d), dtype=torch.bfloat16 if dtype is None else dtype,
+            k = torch.empty(B, cache.heads, N, cache.d, dtype=torch.bfloat16 if dtype is None else dtype,
                             device=cache.device)
-        kB, H, kN, dt = _kv4_rows(k, "k", cache)
-        if kB != B or kN != N or H != cache.heads or (dtype is not None and k.dtype is not dtype):
+        shape, kdtype, dt = _kv4_rows(k, "k", cache)
+        if shape[0] != B or shape[2] != N or shape[1] != cache.heads or (dtype is not None and kdtype is not dtype):
             raise ValueError(f"k must be [{B}, {cache.heads}, {N}, {cache.d}]" + ("" if dtype is None else f" of {dtype}"))
         if v is None:
             v = torch.empty_like(k)
-        st = load().attn_kv4_read(cache._addr, bt, sl, first, k.data_ptr(), _kv4_like(v, "v", k), B, N, max_pages, dt, sp)
+            vp = v.data_ptr()
+        else:
+            vp = _kv4_like(v, "v", shape, kdtype, cache)
+        st = load().attn_kv4_read(cache._addr, bt, sl, first, k.data_ptr(), vp, B, N, max_pages, dt, sp)
         if st or check:
             _check(st, "attn_kv4_read")
             _check_device(check, sp, "attn_kv4_read")
@@ -761,21 +765,25 @@ def forward_kv4(q, cache, block_table, seq_lens, q_lens=None, causal=False, scal
     LSE = -inf. `workspace`: a uint8 tensor of at least attn_fwd_kv4_workspace_bytes(...);
     None: one kept per thread, device and stream (inside a graph capture: the graph's own).
     Asynchronous like forward(); bad page numbers and lengths as in kv4_append."""
-    B, Hq, N, dt = _kv4_rows(q, "q", cache)
+    shape, dtype, dt = _kv4_rows(q, "q", cache)
+    B, Hq, N, _ = shape
     bt, max_pages = _kv4_table(block_table, B, cache)
     sl = _kv4_int32(seq_lens, "seq_lens", (B,), cache)
     ql = None if q_lens is None else _kv4_int32(q_lens, "q_lens", (B,), cache)
     sp, place = _kv4_stream(cache, stream)
     try:
         if out is None:
-            out = (torch.empty if q_lens is None else torch.zeros)(q.shape, dtype=q.dtype, device=q.device)
-        o = _kv4_like(out, "out", q)
-        if lse is None:
-            if with_lse:
-                lse = (torch.empty if q_lens is None else torch.zeros)((B, Hq, N), dtype=torch.float32, device=q.device)
-        elif lse.dtype is not torch.float32 or lse.shape != (B, Hq, N) or lse.get_device() != cache._index or \
-                not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(B, Hq, N)} on {cache.device}")
+            out = torch.empty_like(q) if q_lens is None else torch.zeros_like(q)
+            o = out.data_ptr()
+        else:
+            o = _kv4_like(out, "out", shape, dtype, cache)
+        if lse is not None:
+            lp = _kv4_like(lse, "lse", (B, Hq, N), torch.float32, cache)
+        elif with_lse:
+            lse = (torch.empty if q_lens is None else torch.zeros)(B, Hq, N, dtype=torch.float32, device=cache.device)
+            lp = lse.data_ptr()
+        else:
+            lp = None
         sizes = (B, Hq, N, max_pages)
         need = cache._need.get(sizes)
         if need is None:
@@ -787,7 +795,7 @@ def forward_kv4(q, cache, block_table, seq_lens, q_lens=None, causal=False, scal
         elif workspace.get_device() != cache._index or workspace.dtype is not torch.uint8 or \
                 not workspace.is_contiguous() or workspace.numel() < need:
             raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {cache.device}")
-        st = load().attn_fwd_kv4(cache._addr, q.data_ptr(), bt, sl, ql, o, None if lse is None else lse.data_ptr(),
+        st = load().attn_fwd_kv4(cache._addr, q.data_ptr(), bt, sl, ql, o, lp,
                                  None if workspace is None else workspace.data_ptr(),
                                  0 if workspace is None else workspace.numel(), B, Hq, N, max_pages,
                                  0.0 if scale is None else float(scale), 1 if causal else 0, dt, sp)
