@@ -75,13 +75,14 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pa
   return r;
 }
 
-// A kernel that may start while the one before it in the stream runs, and waits for it before it
-// reads what that one wrote.
+// Launches a kernel that may start before the one before it in the stream has ended, and waits for it
+// itself (kv4_grid_wait).
 template <class P>
-cudaError_t launch_after(void (*kern)(P), dim3 grid, int threads, cudaStream_t stream, const P& p) {
+cudaError_t launch_after(void (*kern)(P), dim3 grid, int threads, int smem, cudaStream_t stream, const P& p) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -95,8 +96,9 @@ template <class C, bool F16>
 attn_status launch_kv4_dec(const attn::Kv4AttnParams& p, int tag, cudaStream_t stream) {
   auto kern = attn::kv4_decode_sm100<C, F16>;
   if (!set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, tag)) return ATTN_ERR_CUDA;
-  kern<<<p.ctas, attn::kDecWarps * 32, C::SMEM_BYTES, stream>>>(p);
-  const cudaError_t e = launch_after(attn::kv4_join_sm100<C::D, C::ROWS, F16>, dim3(p.ctas, C::ROWS / 8), 256, stream, p);
+  cudaError_t e = launch_after(kern, dim3(p.ctas), attn::kDecWarps * 32, C::SMEM_BYTES, stream, p);
+  if (e == cudaSuccess)
+    e = launch_after(attn::kv4_join_sm100<C::D, C::ROWS, F16>, dim3(p.ctas, C::ROWS / 8), 256, 0, stream, p);
   if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) {
     forget_smem(tag);
     return ATTN_ERR_CUDA;
@@ -109,9 +111,11 @@ attn_status launch_kv4_chunk(const attn::Kv4AttnParams& p, int tag, cudaStream_t
   using C = attn::Kv4ChunkCfg<D, PAIR>;
   auto kern = attn::kv4_chunk_sm100<C, F16>;
   if (!set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM_BYTES, tag)) return ATTN_ERR_CUDA;
-  kern<<<p.ctas, C::THREADS, C::SMEM_BYTES, stream>>>(attn::Kv4ChunkParams{p, wait_limit, fault_cta});
-  const cudaError_t e = launch_after(attn::kv4_join_sm100<D, attn::kChunkRows, F16>,
-                                     dim3(p.ctas, (PAIR ? 128 : attn::kChunkRows) / 8), 256, stream, p);
+  cudaError_t e = launch_after(kern, dim3(p.ctas), C::THREADS, C::SMEM_BYTES, stream,
+                               attn::Kv4ChunkParams{p, wait_limit, fault_cta});
+  if (e == cudaSuccess)
+    e = launch_after(attn::kv4_join_sm100<D, attn::kChunkRows, F16>,
+                     dim3(p.ctas, (PAIR ? 128 : attn::kChunkRows) / 8), 256, 0, stream, p);
   if (cudaGetLastError() != cudaSuccess || e != cudaSuccess) {
     forget_smem(tag);
     return ATTN_ERR_CUDA;
@@ -150,9 +154,9 @@ attn_status attn_kv4_append(const attn_kv4_cache* cache, const void* k, const vo
   const bool f16 = dtype == ATTN_FP16;
   auto kern = cache->d == 128 ? (f16 ? attn::kv4_append_sm100<128, true> : attn::kv4_append_sm100<128, false>)
                               : (f16 ? attn::kv4_append_sm100<64, true> : attn::kv4_append_sm100<64, false>);
-  kern<<<dim3(static_cast<unsigned>(B * cache->Hkv * p.tiles), 2), attn::kKv4Threads, 0,
-         static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  const cudaError_t e = launch_after(kern, dim3(static_cast<unsigned>(B * cache->Hkv * p.tiles), 2), attn::kKv4Threads, 0,
+                                     static_cast<cudaStream_t>(stream), p);
+  return cudaGetLastError() == cudaSuccess && e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block_table, const int* seq_lens, const int* starts,
@@ -170,9 +174,9 @@ attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block_table, c
   const bool f16 = dtype == ATTN_FP16;
   auto kern = cache->d == 128 ? (f16 ? attn::kv4_read_sm100<128, true> : attn::kv4_read_sm100<128, false>)
                               : (f16 ? attn::kv4_read_sm100<64, true> : attn::kv4_read_sm100<64, false>);
-  kern<<<dim3(static_cast<unsigned>(B * cache->Hkv * p.tiles), 2), attn::kKv4Threads, 0,
-         static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  const cudaError_t e = launch_after(kern, dim3(static_cast<unsigned>(B * cache->Hkv * p.tiles), 2), attn::kKv4Threads, 0,
+                                     static_cast<cudaStream_t>(stream), p);
+  return cudaGetLastError() == cudaSuccess && e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 size_t attn_fwd_kv4_workspace_bytes(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {

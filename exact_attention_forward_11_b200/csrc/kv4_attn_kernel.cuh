@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const uint32_t smem0 = b200::smem_addr(smem_raw);
+  kv4_grid_wait();
   asm volatile("griddepcontrol.launch_dependents;");
   if (tid == 0) p.heads[blockIdx.x].parts = 0;
   const uint32_t ring = smem0 + warp * C::STAGES * C::STAGE;
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
 template <int D, int ROWS, bool F16>
 __global__ void __launch_bounds__(256) kv4_join_sm100(const Kv4AttnParams p) {
   constexpr int E = D / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  kv4_grid_wait();
   const Kv4Head hd = p.heads[blockIdx.x];
   if (hd.parts == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

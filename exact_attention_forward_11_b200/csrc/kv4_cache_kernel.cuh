@@ -16,6 +16,11 @@
 
 namespace attn {
 
+// Every kernel of the cache is launched so that its CTAs may start while the kernel before it in the stream ends, and
+// waits here, before it touches any memory (or allocates tensor memory), until that one is complete: the launch alone
+// overlaps (6 sequences of 2047 keys x 12 heads 14.4 -> 12.3 us a call).
+__device__ __forceinline__ void kv4_grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The cache as every kernel sees it.
 struct Kv4Cache {
   uint8_t* codes[2];         // keys, values: [num_pages, H, page_size, d / 2]
@@ -159,6 +164,7 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_append_sm100(const __grid_con
   constexpr int LPR = D / 16, RPP = 32 / LPR, U = kKv4WarpRows / RPP;   // lanes per row, rows per pass, passes
   const int which = blockIdx.y, lane = threadIdx.x & 31, blk = lane % LPR;
   const int exp2 = which == 0 ? p.c.exp[0] : p.c.exp[1];
+  kv4_grid_wait();
   const Kv4MoveTile tile(p);
   const int r0 = (threadIdx.x >> 5) * kKv4WarpRows;                     // the warp's first row of the tile
   const uint4* src = reinterpret_cast<const uint4*>(which == 0 ? p.in[0] : p.in[1]) + tile.row0 * (LPR * 2) + blk * 2;
@@ -213,6 +219,7 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_sm100(const __grid_const
   constexpr int LPR = D / 8, RPP = 32 / LPR, U = kKv4WarpRows / RPP;
   const int which = blockIdx.y, lane = threadIdx.x & 31, unit = lane % LPR;
   const float up = f32_exp2i(which == 0 ? p.c.exp[0] : p.c.exp[1]);
+  kv4_grid_wait();
   const Kv4MoveTile tile(p);
   const int r0 = (threadIdx.x >> 5) * kKv4WarpRows;
   const int start = p.first != nullptr ? kv4_clamp(p.first[tile.b], p.c.max_pages << p.c.page_shift) : 0;

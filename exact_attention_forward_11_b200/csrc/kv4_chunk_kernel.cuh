@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
   uint32_t* rows = reinterpret_cast<uint32_t*>(smem + C::SMEM_ROWS);      // [RING][128]
   int* edges = reinterpret_cast<int*>(rows + C::RING * 128);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  kv4_grid_wait();
   asm volatile("griddepcontrol.launch_dependents;");
 
   if (threadIdx.x == 0) {

@@ -622,3 +622,38 @@ def test_threads_on_one_stream(cuda_lib):
         assert len(got[t]) == 200
         for o, lse in got[t]:
             assert torch.equal(o, want[t][0]) and torch.equal(lse, want[t][1])
+
+
+def test_graph_with_copies_and_a_fork(cuda_lib):
+    """Captured behind copies, a memset and another stream's append: every call waits for what it reads."""
+    lib, d, lens = cuda_lib, 128, [1500, 900]
+    pg, other = Paged(lib, 2, 2, d, 16, 100, seed=1), Paged(lib, 2, 2, d, 16, 100, seed=2)
+    k, v = fill(pg, lens, torch.bfloat16, 2)
+    q_from, q, n = make_q(2, 4, 1, d, torch.bfloat16, 3), torch.empty(2, 4, 1, d, dtype=torch.bfloat16, device=DEV), ints([0, 0])
+    fill(other, lens, torch.bfloat16, 2)                                   # the expected result, from a second cache
+    want = lib.forward_kv4(q_from, other.cache, other.bt, ints(lens), causal=True, check=True)
+    for t in other.tensors():
+        t.fill_(0xFF)
+    src = ints(lens)
+    side = torch.cuda.Stream()
+    gph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        n.zero_()
+        n.copy_(src)
+        q.copy_(q_from)
+        lib.kv4_append(other.cache, k, v, other.bt, src, new_lens=src, stream=side)
+        first = lib.forward_kv4(q, pg.cache, pg.bt, n, causal=True)
+        main.wait_stream(side)
+        second = lib.forward_kv4(q, other.cache, other.bt, n, causal=True)
+        kr, _ = lib.kv4_read(other.cache, other.bt, n, 1500)
+        back = kr.clone()
+    for _ in range(3):
+        for t in (*other.tensors(), *first, *second, back):
+            t.zero_()
+        gph.replay()
+        torch.cuda.synchronize()
+        for o, lse in (first, second):
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        assert torch.equal(back, lib.kv4_read(pg.cache, pg.bt, src, 1500, check=True)[0])
