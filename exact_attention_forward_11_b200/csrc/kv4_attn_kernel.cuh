@@ -35,10 +35,10 @@
 // Bound: HBM at 4.5 bits a value is 12e12 values / s, 41 per SM and clock; a value costs half a
 // conversion and half a multiplication (64 lanes / clk / SM each), and with everything else 2.3
 // instructions of a lane. Measured (32 sequences of 32768 keys x 8 heads, d = 128, one token, 4 query heads to a key
-// head): 223 us, 5.4 TB/s of the cache's bytes, 0.83 of the measured copy rate, at 64 % of the issue slots;
-// under a power cap the clock falls and with it the rate (258 us). The list of a run starts after about 7 us
+// head): 218 us, 5.5 TB/s of the cache's bytes, 0.84 of the measured copy rate, at 64 % of the issue slots;
+// after a second under the power cap (1.77 instead of 1.965 GHz) 252 us. The list of a run starts after about 7 us
 // (lengths, page numbers, first codes: a chain of three memory latencies) and each further segment costs
-// about 2 us, which is what small batches spend their time on (16 sequences of up to 4096 keys: 24.7 us
+// about 2 us, which is what small batches spend their time on (16 sequences of up to 4096 keys: 23.0 us
 // for 8.1 us of bytes).
 #pragma once
 

@@ -148,8 +148,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // In both kernels a warp moves 8 rows: LPR lanes hold a row, 32 / LPR rows make a pass, and one lane looks up
 // each of the 8 rows. Both are near the bytes they move, and instructions are what is left: with every lane
-// looking up its own row, and quotients rounded in integers, append_prompt (4 x 8 heads x 4096 tokens written
-// and read back) took 38.0 us instead of 34.1 and read_long (8 heads x 32768 tokens) 32.2 instead of 30.6.
+// looking up its own row, and quotients rounded in integers, a prompt (4 x 8 heads x 4096 tokens written
+// and read back) took 38.0 us instead of 34.1 and a read of 8 heads x 32768 tokens 32.2 instead of 30.6 (33.9 and 29.9
+// since the launches overlap).
 constexpr int kKv4WarpRows = kKv4Rows / (kKv4Threads / 32);
 static_assert(kKv4WarpRows == 8, "rows of a warp");
 
@@ -158,7 +159,7 @@ static_assert(kKv4WarpRows == 8, "rows of a warp");
 // a multiple of 2^-16 by adding and subtracting 192, which decides alike: y has at most 11 significant bits and
 // t s at most 7, so q is t itself or at least 2^-11 t >= 2^-13 away from it; 1 / s is off by 2^-24 of
 // itself and the sum rounds by 2^-17, so an exact t comes out as t and nothing crosses one. (Sixteen IEEE
-// divisions a block took 2 us more on append_prompt.)
+// divisions a block took 2 us more on that prompt.)
 template <int D, bool F16>
 __global__ void __launch_bounds__(kKv4Threads) kv4_append_sm100(const __grid_constant__ Kv4MoveParams p) {
   constexpr int LPR = D / 16, RPP = 32 / LPR, U = kKv4WarpRows / RPP;   // lanes per row, rows per pass, passes

@@ -33,7 +33,7 @@
 // over 32768 keys, causal: 1.05 ms, 1010 TFLOP/s, 0.60 of the measured bf16 burst rate (0.72 of the sustained; without
 // the conversion, which is then wrong, 0.96 ms); a step of two row tiles takes 2.3 us, of which a
 // softmax group works 1.5 and waits for its next S the rest. A run starts after 9 us and a further
-// segment costs about 6 us: 4 sequences of 238 to 512 queries x 28 heads over 2109 to 4096 keys take 134 us (500 TFLOP/s).
+// segment costs about 6 us: 4 sequences of 238 to 512 queries x 28 heads over 2109 to 4096 keys take 131 us (510 TFLOP/s).
 #pragma once
 
 #include "attn_fwd_kernel.cuh"
