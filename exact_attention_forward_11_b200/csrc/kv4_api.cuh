@@ -53,22 +53,36 @@ struct Kv4Plan {
   size_t ml_bytes, o_bytes, workspace;
 };
 constexpr int kKv4Sms = 148;
-// Rows of a cached head up to which the decode kernel runs (blocks of 8 or 16 rows; each block reads the
-// keys again, from L2). Both measured: 32 rows over 8 sequences of about 6000 keys x 4 heads 31.9 us here, 41.9 in the
-// chunk kernel; over one sequence of 32768 keys x 8 heads 38.4 and 50.1; 48 rows 46.2 and 48.3; 64 rows 55.9 and 48.7.
-constexpr int kKv4DecodeRows = 32;
+// The kernel, by the rows of a cached head and the work: the decode kernel in blocks of 8 (nt = 1) or 16 rows (2; a
+// block reads the keys again, from L2), or the chunk kernel (0). Work is the units of Kv4Runs at the table's full
+// length, an item counting as its tiles and two. Both sides measured (d = 128, 8 cached heads unless said):
+//   * 9 to 16 and 25 to 32 rows: blocks of 16 (16 sequences of 4000 keys, 16 rows 33.0 us, in blocks of 8 38.4; 32
+//     rows 60 and 69). 17 to 24 rows: three blocks of 8 instead of two of 16 (54.7 and 59.1).
+//   * above 32 rows: the chunk kernel (32 sequences of 8192 keys, 40 rows 219 us and 258; 8 of 6000 keys, 64 rows 60.6 and
+//     76), but the decode kernel for up to 1024 units of 16 rows, where its start is the shorter (6 of 1000 keys, 48 rows:
+//     864 units, 13.5 us and 27.3; 960 units 17.6 and 20.4; 1152 units 22.0 and 24.4, 1536 units 23.0 and 22.8).
+//   * blocks of 8 for any rows up to 512 units of 8 rows (512 units: 8.4 us and 10.4; 768: 14.5 and 13.2).
+constexpr int kKv4DecodeRows = 32, kKv4DecodeUnits = 1024, kKv4SmallUnits = 512;
 
 Kv4Plan kv4_plan(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {
   Kv4Plan r;
   const long long rows = static_cast<long long>(Hq / Hkv) * N;
-  r.nt = rows <= 8 ? 1 : (rows <= kKv4DecodeRows ? 2 : 0);
+  const long long positions = static_cast<long long>(max_pages) * page_size;
+  auto work = [&](int block) {
+    const double item = static_cast<double>((positions + attn::kDecTile - 1) / attn::kDecTile + attn::kDecSegmentTiles);
+    return item * B * Hkv * static_cast<double>((rows + block - 1) / block);
+  };
+  if (rows <= 8 || (rows > 16 && rows <= 24) || work(8) <= kKv4SmallUnits)
+    r.nt = 1;
+  else
+    r.nt = rows <= kKv4DecodeRows || work(16) <= kKv4DecodeUnits ? 2 : 0;
   const int block = r.nt > 0 ? 8 * r.nt : attn::kChunkRows, keys = r.nt > 0 ? attn::kDecTile : 128;
   r.row_blocks = static_cast<int>((rows + block - 1) / block);
-  const long long tiles = (static_cast<long long>(max_pages) * page_size + keys - 1) / keys;
+  const long long tiles = (positions + keys - 1) / keys;
   const long long most = kKv4Sms * (r.nt == 1 ? 2 : 1);
   const double units = static_cast<double>(tiles) * B * Hkv * r.row_blocks;
   r.ctas = static_cast<int>(units < most ? units : most);
-  r.fits = r.nt == 0 || units + static_cast<double>(attn::kDecSegmentTiles) * B * Hkv * r.row_blocks < 2147483648.0;
+  r.fits = r.nt == 0 || work(block) < 2147483648.0;
   r.ml_bytes = static_cast<size_t>(2) * r.ctas * block * sizeof(float2);
   r.o_bytes = static_cast<size_t>(2) * r.ctas * block * d * sizeof(float);
   r.workspace = r.ml_bytes + r.o_bytes + (r.ctas * sizeof(attn::Kv4Head) + 15) / 16 * 16;

@@ -105,9 +105,9 @@ ATTN_API attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block
  *          two host threads make at the same time, on one stream even (a call is two
  *          launches), need separate workspaces.
  *   scale: 0 selects 1/sqrt(d).
- *   Size: with R = Hq / Hkv * N <= 32 rows of a cached head, at most 2^31 tiles of 256
- *          keys: B * Hkv * ceil(R / 8) * (ceil(max_pages * page_size / 256) + 2) < 2^31 (R <= 8;
- *          ceil(R / 16) above), else ATTN_ERR_INVALID_ARG.
+ *   Size: with R = Hq / Hkv * N <= 32 rows of a cached head, fewer than 2^31 tiles of 256 keys:
+ *          B * Hkv * ceil(R / b) * (ceil(max_pages * page_size / 256) + 2) < 2^31 with b = 8
+ *          (R <= 8 and 17 to 24) or 16, else ATTN_ERR_INVALID_ARG.
  * Arithmetic: scores and P V on f16 tensor-core products with fp32 accumulation
  * (every cached value is exact in f16; a query row is scaled by a power of two to
  * f16, P is rounded to f16); softmax statistics in fp32. Repeated calls give

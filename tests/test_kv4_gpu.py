@@ -34,8 +34,19 @@ def n64(t):
     return t.double().cpu().numpy()
 
 
+@pytest.fixture(params=["tight", "room"])
+def room(request):
+    """Block tables as long as the sequences need, and with room for 2^18 more tokens (unset entries): above 32
+    rows of a cached head, the two take different kernels at these sizes."""
+    Paged.room = request.param == "room"
+    yield Paged.room
+    Paged.room = False
+
+
 class Paged:
     """A cache whose pages lie in random order, every unused byte 0xFF (NaN scales, -6 codes)."""
+
+    room = False
 
     def __init__(self, lib, B, H, d, page, max_pages, k_exp=0, v_exp=0, seed=0, spare=2):
         g = torch.Generator().manual_seed(seed)
@@ -45,6 +56,10 @@ class Paged:
         for t in self.tensors():
             t.fill_(0xFF)
         self.bt = torch.randperm(P, generator=g)[:B * max_pages].view(B, max_pages).to(torch.int32).to(DEV)
+        if self.room:
+            more = torch.full((B, (1 << 18) // page), -1, dtype=torch.int32, device=DEV)
+            self.bt = torch.cat([self.bt, more], 1).contiguous()
+            self.max_pages = self.bt.shape[1]
 
     def tensors(self):
         c = self.cache
@@ -206,6 +221,9 @@ ATTN_CASES = [
     (128, 5, 5, 16, torch.bfloat16, 257, [300], None, True, (0, 0)),
     (64, 8, 8, 16, torch.bfloat16, 65, [65, 64, 200], [65, 64, 1], True, (0, 0)),
     (128, 2, 1, 65536, torch.float16, 200, [1025], None, True, (0, 0)),                 # one page holds everything
+    (64, 6, 3, 16, torch.bfloat16, 300, [310, 900], [300, 7], True, (0, 0)),            # more rows than a tile has keys
+    (128, 6, 2, 16, torch.float16, 7, [600, 5], None, True, (0, 0)),                    # 21 rows
+    (128, 4, 2, 32, torch.bfloat16, 300, [40, 0, 299], [300, 300, 299], True, (0, 0)),  # rows before the first key
 ]
 
 
@@ -216,6 +234,7 @@ def make_q(B, Hq, N, d, dt, seed):
     return q.to(dt).to(DEV)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("d,Hq,Hkv,page,dt,N,lens,qlens,causal,exps", ATTN_CASES)
 def test_attention(cuda_lib, d, Hq, Hkv, page, dt, N, lens, qlens, causal, exps):
     lib, B = cuda_lib, len(lens)
@@ -242,6 +261,7 @@ def test_attention(cuda_lib, d, Hq, Hkv, page, dt, N, lens, qlens, causal, exps)
     assert none is None and torch.equal(o3, o2)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("scale", [0.03, 1.0])
 def test_attention_scale_and_long_rows(cuda_lib, scale):
     """A given scale; rows peaked on few keys (the running maximum moves often) and a longer cache."""
@@ -276,6 +296,7 @@ def test_extreme_queries(cuda_lib):
     check_attention(o, lse, q[:, 3:4], pg, [300], [1], False)
 
 
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("N,Hq", [(1, 4), (6, 2), (140, 1)])
 @pytest.mark.parametrize("which", ["k", "v"])
 def test_nan_in_the_cache(cuda_lib, N, Hq, which):
@@ -362,6 +383,7 @@ def test_offsets_past_32_bits(cuda_lib):
 
 
 # ---------------------------------------------------------------- streams, graphs, a run of them together
+@pytest.mark.usefixtures("room")
 @pytest.mark.parametrize("N,L", [(1, 2000), (4, 900), (150, 700)])
 def test_streams_and_graphs(cuda_lib, N, L):
     """On a side stream; captured, with changed inputs and lengths at replay; two graphs replayed in
@@ -454,6 +476,7 @@ def test_decoding_run(cuda_lib):
             assert (kv4_rows(sf.cpu().numpy(), bt, page, 0, lens[b]) == s).all()
 
 
+@pytest.mark.usefixtures("room")
 def test_one_workspace_for_calls_of_every_shape(cuda_lib):
     """A caller's workspace, full of anything, used by calls of different shapes in turn: the results
     are those of the binding's own, and nothing behind the required size is written."""
@@ -495,6 +518,7 @@ def test_many_sequences(cuda_lib, N):
     check_attention(o, lse, big, pg, lens, [min(150, x) for x in lens], True, rows=(0, 1, 40, 149))
 
 
+@pytest.mark.usefixtures("room")
 def test_debug_build_is_bit_identical(cuda_lib):
     """The debug build's cache calls give the release build's bits, and report a bad page with its site."""
     lib, d = cuda_lib, 128
@@ -657,3 +681,44 @@ def test_graph_with_copies_and_a_fork(cuda_lib):
         for o, lse in (first, second):
             assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
         assert torch.equal(back, lib.kv4_read(pg.cache, pg.bt, src, 1500, check=True)[0])
+
+
+@pytest.mark.parametrize("N", [40, 140])
+def test_bad_tables_in_long_chunks(cuda_lib, N):
+    """The same errors of tables and lengths in the kernel that long tables take."""
+    lib, d, lens = cuda_lib, 128, [200, 160, 150]
+    Paged.room = True
+    try:
+        pg = Paged(lib, 3, 2, d, 16, 13, seed=6)
+    finally:
+        Paged.room = False
+    fill(pg, lens, torch.bfloat16, 8)
+    q = make_q(3, 4, N, d, torch.bfloat16, 9)
+    good, gl = lib.forward_kv4(q, pg.cache, pg.bt, ints(lens), check=True)
+    bad_bt, missing = pg.bt.clone(), [200, 250, 150]                  # pages past 13 are unset (-1)
+    bad_bt[1, 2] = 1 << 30
+    for bt, sl, ql in ((bad_bt, lens, None), (pg.bt, [200, -5, 150], None), (pg.bt, missing, None),
+                       (pg.bt, lens, [N, N + 1, N]), (pg.bt, lens, [N, -1, N])):
+        o, lse = lib.forward_kv4(q, pg.cache, bt, ints(sl), q_lens=None if ql is None else ints(ql))
+        torch.cuda.synchronize()
+        assert lib.attn_get_device_status(None) == lib.ATTN_ERR_BOUNDS
+        assert lib.attn_get_device_status(None) == lib.ATTN_OK
+        for b in (0, 2):
+            assert torch.equal(o[b], good[b]) and torch.equal(lse[b], gl[b])
+
+
+def test_plans_agree(cuda_lib):
+    """Short chunks with a tight table and with room (two kernels, three block heights): each within the
+    tolerance, and every row written."""
+    lib, d = cuda_lib, 128
+    for N, Hq in ((40, 2), (100, 2), (300, 4), (12, 6)):
+        lens = [N + 300, N, 3]
+        pg = Paged(lib, 3, 2, d, 16, (N + 300 + 15) // 16, seed=N)
+        fill(pg, lens, torch.bfloat16, N)
+        wide = torch.cat([pg.bt, torch.full((3, 1 << 14), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
+        q = make_q(3, Hq, N, d, torch.bfloat16, N)
+        for bt in (pg.bt, wide):
+            out, lse = torch.full_like(q, float("nan")), torch.full((3, Hq, N), float("nan"), device=DEV)
+            lib.forward_kv4(q, pg.cache, bt, ints(lens), causal=True, out=out, lse=lse, check=True)
+            assert not torch.isnan(out).any() and not torch.isnan(lse).any()
+            check_attention(out, lse, q, pg, lens, [N] * 3, True, rows=(0, 1, N // 2, N - 1))
