@@ -24,7 +24,7 @@
 // units), so most steps cost one vote and no reduction across lanes; P <= 2^8 then, well inside f16.
 //
 // Schedule: the 256-key tiles of all (b, h, row block) make one long list that is cut into
-// equal runs, one per CTA, so uneven lengths balance without the host knowing them. A run
+// runs, one per CTA (Kv4Runs), so uneven lengths balance without the host knowing them. A run
 // that covers part of a (b, h, row block) writes its unnormalised O, maximum and sum to the
 // workspace (two slots per CTA: a run's first and last item); kv4_join_sm100 joins the parts in
 // the order of the runs, so results do not depend on timing. It is launched with programmatic
