@@ -619,16 +619,13 @@ attn_status attn_bwd(const void* q, const void* k, const void* v, const void* o,
 
 namespace {
 
-constexpr int kW4MaxCtas = 296;      // two per SM of a B200: the most a split-K launch uses
 constexpr int kW4MinSlices = 8;      // a split-K run covers at least this many 128-deep slices
 
 // Split-K CTA cap for U units, before the device's SM count is applied.
 int w4_cta_cap(long long units) {
   const long long c = units / kW4MinSlices;
-  return static_cast<int>(c < 1 ? 1 : (c > kW4MaxCtas ? kW4MaxCtas : c));
+  return static_cast<int>(c < 1 ? 1 : (c > attn::kW4MaxCtas ? attn::kW4MaxCtas : c));
 }
-
-size_t w4_tickets_bytes(int N) { return static_cast<size_t>((16ll * (N / 128) + 255) / 256 * 256); }
 
 attn_status w4_check(const void* x, const void* qweight, const void* scales, const void* zeros, const void* y, int M,
                      int N, int K) {
@@ -667,7 +664,7 @@ attn_status launch_w4(const void* x, const void* qweight, const void* scales, co
   p.y = static_cast<__half*>(y);
   p.tickets = ws == nullptr ? nullptr : static_cast<uint32_t*>(ws);
   p.part = ws == nullptr ? nullptr
-                         : reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w4_tickets_bytes(N));
+                         : reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + attn::w4_partials_offset(N));
   p.timeout_cycles = kWaitLimitCycles;
   attn::w4a16_gemm_sm100<<<ctas, C::THREADS, smem, stream>>>(tx, tw, ts, tz, p);
   if (cudaGetLastError() != cudaSuccess) {
@@ -690,9 +687,8 @@ size_t w4a16_gemm_splitk_workspace_bytes(int M, int N, int K) {
   using C = attn::W4Cfg;
   if (M < 1 || N < 1 || K < 1 || M > C::MAX_M || N % C::BN != 0 || K % C::GROUP != 0) return 0;
   if (static_cast<long long>(K) * N >= (1ll << 40)) return 0;
-  const long long mpad = (M + 15) / 16 * 16;
   const int cap = w4_cta_cap(static_cast<long long>(N / C::BN) * (K / C::GROUP));
-  return w4_tickets_bytes(N) + static_cast<size_t>(2ll * cap * mpad * C::BN * 4);
+  return attn::w4_workspace_bytes(N, (M + 15) / 16 * 16, cap);
 }
 
 attn_status w4a16_gemm_splitk(const void* x, const void* qweight, const void* scales, const void* zeros, void* y,

@@ -20,7 +20,8 @@
 // slot (2c for the run's first tile, 2c+1 for its last); the warp that takes the
 // last ticket of its tile's 32-column quarter adds the tile's partials in CTA
 // order (so the sum does not depend on which CTA finishes last), writes Y and
-// resets the ticket. The MMA is issued with the operands swapped
+// resets the ticket. Tickets lie at the same place for every N (w4_ticket), so that
+// calls of different sizes can share a workspace. The MMA is issued with the operands swapped
 // (D[128 columns n][M tokens] = W^T X^T) so that M = 128 is the weight side and
 // the token count only sets the MMA's N (padded to a multiple of 16). The
 // dequantised weights go straight from registers into tensor memory (one thread
@@ -101,7 +102,7 @@ struct W4Params {
   long long units;           // U = (N / 128) * (K / 128)
   __half* y;                 // [M, N]
   float* part;               // [2 C][mpad][128] fp32 segment partials (split-K only)
-  uint32_t* tickets;         // [4 N / 128] per tile quarter, zero between launches (split-K only)
+  uint32_t* tickets;         // [4 C], see w4_ticket, zero between launches (split-K only)
   uint64_t timeout_cycles;
 };
 
@@ -111,6 +112,27 @@ __host__ __device__ __forceinline__ long long w4_unit0(int c, long long U, int C
 }
 __host__ __device__ __forceinline__ int w4_cta_of(long long u, long long U, int C) {
   return static_cast<int>(((u + 1) * C - 1) / U);
+}
+
+// Split-K workspace: tickets, then partial slots. A tile that several runs share is the last tile
+// of the run that begins it, so the CTA of that run, c_lo, names it: four tickets a CTA, in the
+// workspace's first bytes whatever N is. No call's partials reach into them, else a call of another N
+// would find a partial where it expects a zero ticket.
+constexpr int kW4MaxCtas = 296;               // two per SM of a B200: the most a split-K launch uses
+constexpr size_t kW4TicketBytes = (16 * kW4MaxCtas + 255) / 256 * 256;
+__host__ __device__ __forceinline__ int w4_ticket(int c_lo, int quarter) { return 4 * c_lo + quarter; }
+// What the workspace's size counts before the slots: 16 bytes per tile, which a call leaves as they were.
+__host__ __device__ __forceinline__ size_t w4_front_bytes(int N) {
+  return (static_cast<size_t>(N / W4Cfg::BN) * 16 + 255) / 256 * 256;
+}
+// The slots begin behind both. Where the tickets are the longer part, the excess fits: slot 2 C - 1 is
+// never written (the last run ends with its tile), and a slot has 8192 bytes or more.
+static_assert(kW4TicketBytes - 256 <= 16 * W4Cfg::BN * 4, "tickets within the unused slot");
+__host__ __device__ __forceinline__ size_t w4_partials_offset(int N) {
+  return w4_front_bytes(N) > kW4TicketBytes ? w4_front_bytes(N) : kW4TicketBytes;
+}
+__host__ __device__ __forceinline__ size_t w4_workspace_bytes(int N, int mpad, int ctas) {
+  return w4_front_bytes(N) + static_cast<size_t>(2) * ctas * mpad * W4Cfg::BN * 4;
 }
 
 __global__ void __launch_bounds__(W4Cfg::THREADS, 2)
@@ -333,7 +355,7 @@ __global__ void __launch_bounds__(W4Cfg::THREADS, 2)
       const bool whole = c_lo == c_hi;
       const bool col_ok = dbg_ok(n0 + t < p.N, kSiteW4Out, static_cast<unsigned>(n0 + t));
       const int slot = 2 * static_cast<int>(blockIdx.x) + (tile == tile0 ? 0 : 1);
-      const bool part_ok = whole || dbg_ok(slot < 2 * p.ctas && tile < p.N / C::BN, kSiteW4Split,
+      const bool part_ok = whole || dbg_ok(slot < 2 * p.ctas - 1 && tile < p.N / C::BN, kSiteW4Split,
                                            static_cast<unsigned long long>(slot));
       float* mine = whole ? nullptr : p.part + static_cast<size_t>(slot) * mpad * C::BN;
       for (int c0 = 0; c0 < mpad; c0 += 16) {
@@ -360,7 +382,7 @@ __global__ void __launch_bounds__(W4Cfg::THREADS, 2)
       __threadfence();
       __syncwarp();
       uint32_t prev = 0;
-      uint32_t* ticket = p.tickets + 4 * tile + wq;
+      uint32_t* ticket = p.tickets + w4_ticket(c_lo, wq);
       if (lane == 0) prev = atomicAdd(ticket, 1u);
       prev = __shfl_sync(0xffffffffu, prev, 0);
       if (prev != static_cast<uint32_t>(c_hi - c_lo)) continue;

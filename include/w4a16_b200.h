@@ -57,11 +57,13 @@ ATTN_API attn_status w4a16_gemm(const void* x, const void* qweight, const void* 
  *   workspace       : device memory of at least
  *                     w4a16_gemm_splitk_workspace_bytes(M, N, K) bytes, 16-byte
  *                     aligned, owned by the caller. Zero it once after
- *                     allocating it: its first 16 * N / 128 bytes are tickets
- *                     that every call finds zero and leaves zero. After a call
- *                     whose device status is not ATTN_OK (a pipeline timeout),
- *                     zero it again before its next use. Calls that overlap on
- *                     the GPU need separate workspaces.
+ *                     allocating it: its first 4864 bytes hold tickets that
+ *                     every call finds zero and leaves zero. Calls of any
+ *                     shapes may use one workspace in turn, as long as it is
+ *                     large enough for each. After a call whose device status
+ *                     is not ATTN_OK (a pipeline timeout), zero it again before
+ *                     its next use. Calls that overlap on the GPU need separate
+ *                     workspaces.
  *   workspace_bytes : its size in bytes.
  * Other arguments, layouts and errors as for w4a16_gemm, plus
  * ATTN_ERR_INVALID_ARG for a null workspace or one smaller than required.
@@ -72,7 +74,7 @@ ATTN_API attn_status w4a16_gemm_splitk(const void* x, const void* qweight, const
                                        void* stream);
 
 /* w4a16_gemm_splitk_workspace_bytes - workspace w4a16_gemm_splitk needs for
- * this shape: the tickets (16 bytes per 128 columns, rounded up to 256 bytes)
+ * this shape: 16 bytes per 128 columns, rounded up to 256 bytes,
  * and two fp32 partial slots of M (rounded up to 16) x 128 values per CTA, for
  * at most 296 CTAs (two per SM of a B200). 0 for an invalid or unsupported
  * shape. Host only; launches nothing. */
