@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(256) kv4_join_sm100(const Kv4AttnParams p) {
       return static_cast<size_t>(i == 0 ? hd.slot : 2 * (static_cast<int>(blockIdx.x) + i)) * ROWS + r;
     };
     const int i = i0 + lane;
-    const float2 x = i < hd.parts ? __ldcg(p.part_ml + at(i)) : make_float2(-INFINITY, 0.f);
+    const float2 x = i < hd.parts ? p.part_ml[at(i)] : make_float2(-INFINITY, 0.f);
     float mx = x.x;
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(256) kv4_join_sm100(const Kv4AttnParams p) {
       const bool have = (full >> k) & 1u;
       const float* src = p.part_o + at(i0 + k) * D + lane;
 #pragma unroll
-      for (int e = 0; e < E; ++e) a[e] += f * (have ? __ldcg(src + 32 * e) : 0.f);
+      for (int e = 0; e < E; ++e) a[e] += f * (have ? src[32 * e] : 0.f);
     }
     M = Mn;
   }

@@ -500,11 +500,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
       if (row != kNoRow) {
         const uint4* src = reinterpret_cast<const uint4*>(p.c.codes[0] + static_cast<size_t>(row) * C::CODE_ROW);
 #pragma unroll
-        for (int i = 0; i < NW; ++i) kw[i] = __ldg(src + i);
+        for (int i = 0; i < NW; ++i) kw[i] = src[i];
 #pragma unroll
         for (int i = 0; i < SfWords<D>::N; ++i) {
-          ksf[i] = __ldg(reinterpret_cast<const uint32_t*>(p.c.sf[0] + static_cast<size_t>(row) * C::SF_ROW) + i);
-          vsf_next[i] = __ldg(reinterpret_cast<const uint32_t*>(p.c.sf[1] + static_cast<size_t>(row) * C::SF_ROW) + i);
+          ksf[i] = reinterpret_cast<const uint32_t*>(p.c.sf[0] + static_cast<size_t>(row) * C::SF_ROW)[i];
+          vsf_next[i] = reinterpret_cast<const uint32_t*>(p.c.sf[1] + static_cast<size_t>(row) * C::SF_ROW)[i];
         }
       }
       return true;
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
       if (row != kNoRow) {
         const uint4* src = reinterpret_cast<const uint4*>(p.c.codes[1] + static_cast<size_t>(row) * C::CODE_ROW);
 #pragma unroll
-        for (int i = 0; i < NW; ++i) vw[i] = __ldg(src + i);
+        for (int i = 0; i < NW; ++i) vw[i] = src[i];
       }
     };
     // a row of D f16 values, written to row kr of the tile at dst
