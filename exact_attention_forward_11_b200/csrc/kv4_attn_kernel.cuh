@@ -20,8 +20,12 @@
 // 16-key group is contiguous in its page: nine 16-byte copies per lane and step, two address
 // computations per group and tensor; bulk copies issued by eight lanes cost more instructions,
 // since each lane's copy is issued in turn) and keeps its own running maximum, sum and O; warps meet
-// only where a segment ends. The maximum moves only when a score exceeds it by more than 8 (log2
-// units), so most steps cost one vote and no reduction across lanes; P <= 2^8 then, well inside f16.
+// only where a segment ends. What is subtracted moves only when a score exceeds it by more than 15 (log2
+// units), and then to 7 below that score (kv4_below), so most steps cost one vote and no reduction across lanes, and
+// a row's largest P lies between 2^7 and 2^15: inside f16, with the binades below it left to small
+// probabilities (a row with one key far above the rest has thousands of them: with the maximum itself
+// subtracted, P below 2^-25 were lost from O but not from the sum). They keep 11 bits down to 2^-21 of the row's largest and
+// none is lost above 2^-32 of it.
 //
 // Schedule: the 256-key tiles of all (b, h, row block) make one long list that is cut into
 // runs, one per CTA (Kv4Runs), so uneven lengths balance without the host knowing them. A run
@@ -84,7 +88,7 @@ struct Kv4AttnParams {
   float* lse;                // or nullptr
   const int* q_lens;         // or nullptr
   float* part_o;             // workspace: [2 ctas][ROWS][D]
-  float2* part_ml;           // [2 ctas][ROWS] (maximum in log2 units, sum)
+  float2* part_ml;           // [2 ctas][ROWS] (the value subtracted, in log2 units; sum)
   Kv4Head* heads;            // [ctas]
   int Hq, N, causal;
   int row_blocks;            // ceil(Hq / Hkv * N / ROWS)
@@ -193,6 +197,11 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
 }
 // whether one of the four scale bytes is a NaN
 __device__ __forceinline__ bool any_nan_scale(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u; }
+
+constexpr float kPShift = 7.f, kPRoom = 8.f;         // log2 of the largest P where the subtracted value is set, and its growth
+// The value that is subtracted for a row whose largest score so far (log2 units) is x, and when a score is out of reach.
+__device__ __forceinline__ float kv4_below(float x) { return x - kPShift; }
+__device__ __forceinline__ bool kv4_outgrown(float x, float m) { return x > m + (kPShift + kPRoom); }
 
 // A query row's exponent: q 2^-e lies below 2^10 in magnitude and its largest value at or above 2^9
 // (rows of zeros and of very small values: as far as an fp32 power of two goes; a row with an
@@ -540,7 +549,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           mx[nt][j] = cs[nt][j] * fmaxf(fmaxf(s[0][nt][j], s[0][nt][j + 2]), fmaxf(s[1][nt][j], s[1][nt][j + 2]));
-          grow = grow || mx[nt][j] > m[nt][j] + 8.f;
+          grow = grow || kv4_outgrown(mx[nt][j], m[nt][j]);
         }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -550,7 +559,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
             float x = mx[nt][j];
 #pragma unroll
             for (int sft = 4; sft < 32; sft <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, sft));
-            const float mn = fmaxf(m[nt][j], x);
+            const float mn = fmaxf(m[nt][j], kv4_below(x));
             const float al = mn == -INFINITY ? 1.f : b200::ex2_approx(m[nt][j] - mn);
             m[nt][j] = mn;
             l[nt][j] *= al;

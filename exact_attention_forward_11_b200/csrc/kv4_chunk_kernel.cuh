@@ -58,7 +58,6 @@ struct Kv4ChunkCfg {
   static constexpr uint32_t REGS_SOFTMAX = 184, REGS_CONV = 96, REGS_MMA = 48;
   static_assert(2 * REGS_SOFTMAX + REGS_CONV + REGS_MMA <= 512, "register split");
   static constexpr uint32_t TMEM_COLS = 512, O_COL0 = 256;
-  static constexpr float RESCALE_THRESHOLD = 8.0f;
   static constexpr int SMEM_Q = 0;                              // 2 tiles
   static constexpr int SMEM_K = 2 * TILE_BYTES;                 // 2 buffers
   static constexpr int SMEM_V = 4 * TILE_BYTES;                 // 2 buffers
@@ -690,7 +689,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         }
         const float m_blk = row_max128(sr) * c;
         float m_use = m_run;
-        if (m_blk - m_run > C::RESCALE_THRESHOLD) m_use = m_blk;
+        if (kv4_outgrown(m_blk, m_run)) m_use = kv4_below(m_blk);
         const bool moved = m_use != m_run;
         const float alpha = moved ? ex2_approx(m_run - m_use) : 1.f;
         if (j > j0 && __any_sync(0xffffffffu, moved)) {

@@ -110,7 +110,9 @@ ATTN_API attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block
  *          (R <= 8 and 17 to 24) or 16, else ATTN_ERR_INVALID_ARG.
  * Arithmetic: scores and P V on f16 tensor-core products with fp32 accumulation
  * (every cached value is exact in f16; a query row is scaled by a power of two to
- * f16, P is rounded to f16); softmax statistics in fp32. Repeated calls give
+ * f16; P is rounded to f16, a row's largest between 2^7 and 2^15, so that probabilities
+ * keep 11 bits down to 2^-21 of the row's largest, and none above 2^-32 of it is lost);
+ * softmax statistics in fp32. Repeated calls give
  * bit-identical results.
  */
 ATTN_API attn_status attn_fwd_kv4(const attn_kv4_cache* cache, const void* q, const int* block_table,

@@ -1,0 +1,98 @@
+"""Rows with attention sinks, infinities and NaN over the 4-bit cache, against the fp64 oracle.
+
+Tolerance: that of tests/test_kv4_gpu.py with the rounding of P stated from its range. The kernels keep a
+row's largest P at 2^7 or more, so that what f16 loses of a P below its normal range, 2^-25, is at most
+2^-32 of the row's largest probability p_max:
+    |O - ref| <= eps/2 |ref| + (2^-11 + 2 ds' + 2^-21 + 2 (L/8 + 64) 2^-24) A + L 2^-32 p_max max|v|
+with p_max relative to the row's sum, A and ds' as there, and half a step of fp16's subnormals, 2^-25, for fp16 outputs.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle.kv4 import kv4_attention
+from test_kv4_gpu import DEV, Paged, fill, ints, make_q, n64
+
+pytestmark = pytest.mark.gpu
+
+# rows of a cached head per kernel form: blocks of 8 and of 16 rows, one row tile, two row tiles
+FORMS = {"block8": (1, 4), "block16": (4, 4), "one_tile": (20, 4), "two_tiles": (100, 4)}
+
+
+def check_rows(o, lse, q, pg, lens, causal, rows):
+    eps, tiny = torch.finfo(o.dtype).eps, 2.0 ** -25 if o.dtype == torch.float16 else 0.0
+    o64, l64, q64, scale = n64(o), n64(lse), n64(q), 1 / math.sqrt(pg.d)
+    worst = 0.0
+    for b in range(pg.B):
+        L, n = lens[b], q64.shape[2]
+        k, v = pg.values(b, L)
+        ro, rl = kv4_attention(q64[b], k, v, n, causal, scale)
+        G = q64.shape[1] // pg.H
+        for h in range(q64.shape[1]):
+            for i in [r for r in rows if r < n]:
+                vis = L - n + i + 1 if causal else L
+                kk, vv = k[h // G][:vis], v[h // G][:vis]
+                s = scale * kk @ q64[b, h, i]
+                p = np.exp(s - rl[h, i])
+                ds = (pg.d + 8) * 2.0 ** -23 * scale * (np.abs(kk) @ np.abs(q64[b, h, i])).max() + 2.0 ** -22 * np.abs(s).max()
+                add = (vis / 8 + 64) * 2.0 ** -24
+                bound = eps / 2 * np.abs(ro[h, i]) + (2.0 ** -11 + 2 * ds + 2.0 ** -21 + 2 * add) * (p @ np.abs(vv)) \
+                    + vis * 2.0 ** -32 * p.max() * np.abs(vv).max() + tiny
+                err = np.abs(o64[b, h, i] - ro[h, i])
+                worst = max(worst, (err / bound).max())
+                assert (err <= bound).all(), (b, h, i, err.max(), np.abs(ro[h, i]).max(), (err / bound).max())
+                assert abs(l64[b, h, i] - rl[h, i]) <= ds + add + 2.0 ** -21 + 2.0 ** -22 * abs(rl[h, i])
+    return worst
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("d,dt", [(128, torch.bfloat16), (64, torch.bfloat16), (128, torch.float16)])
+@pytest.mark.parametrize("margin,every,sink", [(18.5, 32, 0.0), (15.0, 32, 0.01), (18.5, 1 << 30, 0.0), (12.0, 32, 0.0),
+                                               (21.0, 32, 0.0)])
+def test_attention_sinks(cuda_lib, form, d, dt, margin, every, sink):
+    """Keys whose score lies `margin` above all others and whose value is zero or small (every 32nd key, or the first
+    alone): what is left of O is the many small probabilities."""
+    lib, H, (N, Hq) = cuda_lib, 1, FORMS[form]
+    lens = [2300, 700]
+    pg = Paged(lib, 2, H, d, 16, 144, seed=7)
+    if form == "one_tile":                                      # a table with room: the kernel of long chunks
+        pg.bt = torch.cat([pg.bt, torch.full((2, 1 << 14), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
+    g = torch.Generator().manual_seed(int(margin * 10) + d)
+    L = max(lens)
+    k = torch.randn((2, H, L, d), generator=g) * 0.3
+    v = 1.0 + 0.3 * torch.randn((2, H, L, d), generator=g)
+    q = torch.randn((2, Hq, N, d), generator=g)
+    q[..., 0] = 16.0
+    k[..., 0] = 0.0
+    k[:, :, ::every, 0] = margin * math.sqrt(d) / 16.0
+    v[:, :, ::every] *= sink
+    q = q.to(dt).to(DEV)
+    lib.kv4_append(pg.cache, k.to(dt).to(DEV), v.to(dt).to(DEV), pg.bt, ints(lens), new_lens=ints(lens), check=True)
+    o, lse = lib.forward_kv4(q, pg.cache, pg.bt, ints(lens), causal=N > 1, check=True)
+    check_rows(o, lse, q, pg, lens, N > 1, (0, 1, N // 2, N - 1))
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_maximum_far_along_the_row(cuda_lib, form):
+    """Scores that rise along the keys in steps on both sides of the threshold at which the running maximum moves,
+    and fall again: P stays inside f16 and nothing of what came before is lost."""
+    lib, d, (N, Hq) = cuda_lib, 128, FORMS[form]
+    for step in (0.9, 4.9, 5.1, 7.0, 9.9, 10.6, 30.0):                     # in natural units, every 160 keys
+        lens = [1300]
+        pg = Paged(lib, 1, 1, d, 16, 82, seed=3)
+        if form == "one_tile":
+            pg.bt = torch.cat([pg.bt, torch.full((1, 1 << 14), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
+        g = torch.Generator().manual_seed(int(step * 10))
+        k, v = torch.randn((1, 1, 1300, d), generator=g) * 0.3, torch.randn((1, 1, 1300, d), generator=g)
+        level = (torch.arange(1300) // 160).float()
+        level = torch.where(level > 5, 10 - level, level)
+        k[..., 0] = step * level * math.sqrt(d) / 16.0
+        q = torch.randn((1, Hq, N, d), generator=g)
+        q[..., 0] = 16.0
+        q = q.to(torch.bfloat16).to(DEV)
+        lib.kv4_append(pg.cache, k.to(torch.bfloat16).to(DEV), v.to(torch.bfloat16).to(DEV), pg.bt, ints(lens),
+                       new_lens=ints(lens), check=True)
+        o, lse = lib.forward_kv4(q, pg.cache, pg.bt, ints(lens), causal=N > 1, check=True)
+        check_rows(o, lse, q, pg, lens, N > 1, (0, 1, N // 2, N - 1))
