@@ -71,7 +71,8 @@ struct Kv4DecCfg {
   static_assert(8 * O_LD * 4 <= STAGE && STAGES >= NT + 2, "merge stages");
   static constexpr int SMEM_ML = RING;             // [warps][ROWS] (max, sum)
   static constexpr int KSTEPS = D / 16;
-  static constexpr int SMEM_BYTES = SMEM_ML + kDecWarps * ROWS * 8;
+  static constexpr int SMEM_NAN = SMEM_ML + kDecWarps * ROWS * 8;   // a word per thread: see nan_rows
+  static constexpr int SMEM_BYTES = SMEM_NAN + kDecWarps * 32 * 4;
   static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 233472, "shared memory per SM");
 };
 
@@ -195,8 +196,20 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-// whether one of the four scale bytes is a NaN
-__device__ __forceinline__ bool any_nan_scale(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u; }
+// 0xFF for each of the four scale bytes that is a NaN
+__device__ __forceinline__ uint32_t nan_scales(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
+
+// Blocks of a value row (its number in the cache) whose scale is a NaN, a bit each.
+template <int D>
+__device__ __forceinline__ uint32_t kv4_nan_blocks(const uint8_t* sf, uint32_t row) {
+  uint32_t blocks = 0u;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(sf + static_cast<size_t>(row) * (D / 16))[i];
+    blocks |= (((nan_scales(w) & 0x01010101u) * 0x01020408u) >> 24) << (4 * i);   // the product gathers the four bits
+  }
+  return blocks;
+}
 
 constexpr float kPShift = 7.f, kPRoom = 8.f;         // log2 of the largest P where the subtracted value is set, and its growth
 // The value that is subtracted for a row whose largest score so far (log2 units) is x, and when a score is out of reach.
@@ -452,6 +465,10 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
       }
     }
     const int lim_all = p.causal ? len - n : len - 1;       // every row sees the keys up to here
+    // bits 2 nt + j: this lane's rows and channels that a NaN value belongs in which the product takes as zero (see the
+    // masks; in shared memory, since it is rare: O made NaN in the step itself cost 2 % on 32 sequences of 32768 keys)
+    uint32_t* const nan_rows = reinterpret_cast<uint32_t*>(smem_raw + C::SMEM_NAN) + tid;
+    *nan_rows = 0u;
     float o[NT][D / 16][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -520,25 +537,41 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
         bool bad;
         if constexpr (D == 128) {
           const uint2 x = *reinterpret_cast<const uint2*>(st + C::ST_VS + lane * 8);
-          bad = any_nan_scale(x.x) || any_nan_scale(x.y);
+          bad = (nan_scales(x.x) | nan_scales(x.y)) != 0u;
         } else {
-          bad = any_nan_scale(*reinterpret_cast<const uint32_t*>(st + C::ST_VS + lane * 4));
+          bad = nan_scales(*reinterpret_cast<const uint32_t*>(st + C::ST_VS + lane * 4)) != 0u;
         }
         vnan = __ballot_sync(0xffffffffu, bad);
+        auto limit = [&](int nt, int j) {           // a row's last visible key, from `base`
+          const int rr = rb * ROWS + nt * 8 + 2 * t + j;
+          return (p.causal ? len - n + rr % p.N : len - 1) - base;
+        };
+        // P = 0 would not keep a NaN value from a row that does not see it: such values count as zero in this
+        // step (below), and the rows that see them are noted: their O becomes NaN where the segment ends (a lane's
+        // channels lie in one block; rows see prefixes, so the first such key decides)
+        if (vnan != 0u) {
+          int first = kDecKeys;
+          for (uint32_t rest = vnan; rest != 0u; rest &= rest - 1u) {
+            const int k = __ffs(rest) - 1;
+            if ((st[C::ST_VS + k * C::SF_ROW + g * C::SF_ROW / 8] & 0x7Fu) == 0x7Fu) first = min(first, k);
+          }
+          if (first < kDecKeys) {
+            uint32_t rows = 0u;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) rows |= first <= limit(nt, j) ? 1u << (2 * nt + j) : 0u;
+            *nan_rows |= rows;
+          }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int rr = rb * ROWS + nt * 8 + 2 * t + j;
-            const int lim = (p.causal ? len - n + rr % p.N : len - 1) - base;   // the row's last visible key
+            const int lim = limit(nt, j);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int k = 8 * i + gk;             // the key of this S^T row
-              float& x = s[i >> 1][nt][2 * (i & 1) + j];
-              // a NaN value reaches the rows that see it through their scores, and no other
-              if ((vnan >> k) & 1u) x = __int_as_float(0x7FC00000);
-              if (k > lim) x = -INFINITY;
-            }
+            for (int i = 0; i < 4; ++i)             // 8 i + gk: the key of this S^T row
+              if (8 * i + gk > lim) s[i >> 1][nt][2 * (i & 1) + j] = -INFINITY;
           }
       }
       // ---- online softmax
@@ -680,6 +713,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
           *reinterpret_cast<float4*>(dst + 4 * i) =
               make_float4(o[nt][2 * i][j], o[nt][2 * i][j + 2], o[nt][2 * i + 1][j], o[nt][2 * i + 1][j + 2]);
       }
+    if (const uint32_t bits = *nan_rows; bits != 0u) {
+      for (int x = 0; x < 2 * NT; ++x) {
+        if (((bits >> x) & 1u) == 0u) continue;
+        float* dst = reinterpret_cast<float*>(smem_raw + warp * C::STAGES * C::STAGE + (x < 2 ? mst[0] : mst[NT - 1])) +
+                     (2 * t + (x & 1)) * C::O_LD + g * (D / 8);
+        for (int i = 0; i < D / 8; ++i) dst[i] = __int_as_float(0x7FC00000);
+      }
+    }
     if (AHEAD && more) load_q(0);
     __syncthreads();
     constexpr int V4 = D / 4;                       // float4 per row

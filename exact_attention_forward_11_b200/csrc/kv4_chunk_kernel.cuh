@@ -68,7 +68,7 @@ struct Kv4ChunkCfg {
   static constexpr int NUM_BARS = 2 * 7 + 4 + 1 + 4 * RING + 2;
   static constexpr int SMEM_MISC = SMEM_BAR + (NUM_BARS + 1) / 2 * 16;
   static constexpr int SMEM_SEG = SMEM_MISC + 16;               // Kv4Seg[RING]
-  static constexpr int SMEM_ROWS = SMEM_SEG + RING * 64;        // [RING][128] cache rows, [RING] first edge key
+  static constexpr int SMEM_ROWS = SMEM_SEG + RING * 64;        // [RING][128] cache rows, [RING] whether there is a tile
   static constexpr int SMEM_XCH = SMEM_ROWS + RING * (128 + 4) * 4;       // PAIR: [128] (max, sum) of group 1
   static constexpr int SMEM_STAGE = SMEM_XCH + 128 * 8;         // output rows: 2 KB per softmax warp
   static constexpr int SMEM_BYTES = SMEM_STAGE + 8 * 2048 + 1024;
@@ -85,7 +85,6 @@ struct __align__(16) Kv4Seg {
   unsigned long long row;    // row of (b, h, 0) in q and o
 };
 static_assert(sizeof(Kv4Seg) <= 64, "segment ring");
-constexpr int kNoTile = static_cast<int>(0x80000000u);
 template <int D>
 struct SfWords { static constexpr int N = D / 64; };   // 32-bit words of a row's scale bytes
 
@@ -95,17 +94,14 @@ struct Kv4ChunkParams {
   int fault_cta;             // testing only: this CTA's walk withholds its first key tile (-1: none)
 };
 
-// Key tiles that the 128 rows from r0 of sequence (len, n) see, and (through `all`) the last key
-// that every valid row among them sees.
-__device__ __forceinline__ int kv4_row_tiles(const Kv4AttnParams& p, int len, int n, int r0, int R, int& all) {
-  all = len - 1;
+// Key tiles that the 128 rows from r0 of sequence (len, n) see.
+__device__ __forceinline__ int kv4_row_tiles(const Kv4AttnParams& p, int len, int n, int r0, int R) {
   if (r0 >= R || n == 0) return 0;
   const int span = min(128, R - r0), i0 = r0 % p.N;
   const bool wraps = i0 + span > p.N;                // the rows reach into the next head
   if (i0 >= n && !wraps) return 0;
   if (!p.causal) return (len + 127) >> 7;
   const int most = i0 < n ? (wraps ? n - 1 : min(n - 1, i0 + span - 1)) : min(n - 1, i0 + span - p.N - 1);
-  all = len - n + (wraps ? 0 : i0);
   return (max(0, min(len, len - n + most + 1)) + 127) >> 7;
 }
 
@@ -127,7 +123,7 @@ struct Kv4ChunkWalk {
   int R;
   long long u, u_end, first;                         // first: first tile of (b, qp)
   long long mine0;                                   // tiles of the lane's (b, qp) entries, from total()
-  int b, qp, h, len, n, kt0, kt1, nkv, lim_all;
+  int b, qp, h, len, n, kt0, kt1, nkv;
   int end[2];
 
   __device__ __forceinline__ explicit Kv4ChunkWalk(const Kv4AttnParams& params)
@@ -137,8 +133,7 @@ struct Kv4ChunkWalk {
   __device__ __forceinline__ int tiles(int idx) {
     const int bb = idx / p.row_blocks, q = idx - bb * p.row_blocks;
     const int l = kv4_len(p.c, bb), nn = kv4_qlen(p, bb);
-    int all;
-    return max(kv4_row_tiles(p, l, nn, q * kChunkRows, R, all), kv4_row_tiles(p, l, nn, q * kChunkRows + 128, R, all));
+    return max(kv4_row_tiles(p, l, nn, q * kChunkRows, R), kv4_row_tiles(p, l, nn, q * kChunkRows + 128, R));
   }
   // total tiles (the whole warp takes part)
   __device__ __forceinline__ long long total(int lane) {
@@ -176,18 +171,16 @@ struct Kv4ChunkWalk {
   }
   // the segment that starts at u (u < u_end); moves u behind it
   __device__ __forceinline__ void next() {
-    int a0, a1;
     for (;;) {
       len = kv4_len(p.c, b);
       n = kv4_qlen(p, b);
-      end[0] = kv4_row_tiles(p, len, n, qp * kChunkRows, R, a0);
-      end[1] = kv4_row_tiles(p, len, n, qp * kChunkRows + 128, R, a1);
+      end[0] = kv4_row_tiles(p, len, n, qp * kChunkRows, R);
+      end[1] = kv4_row_tiles(p, len, n, qp * kChunkRows + 128, R);
       nkv = max(end[0], end[1]);
       if (u < first + static_cast<long long>(nkv) * p.c.H) break;
       first += static_cast<long long>(nkv) * p.c.H;
       if (++qp == p.row_blocks) qp = 0, ++b;
     }
-    lim_all = min(end[0] > 0 ? a0 : len - 1, end[1] > 0 ? a1 : len - 1);
     const uint32_t off = static_cast<uint32_t>(u - first);
     h = static_cast<int>(off / static_cast<uint32_t>(nkv));
     kt0 = static_cast<int>(off - static_cast<uint32_t>(h) * nkv);
@@ -223,10 +216,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
   uint64_t* xch_empty = xch_full + 1;                // and has been read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC);
   uint32_t* abort_word = tmem_slot + 1;
+  volatile uint32_t* zeroed = tmem_slot + 2;         // a NaN value was stored as zero (see the conversion)
   Kv4Seg* segs = reinterpret_cast<Kv4Seg*>(smem + C::SMEM_SEG);
   static_assert(sizeof(Kv4Seg) * C::RING <= C::SMEM_ROWS - C::SMEM_SEG, "segment ring");
   uint32_t* rows = reinterpret_cast<uint32_t*>(smem + C::SMEM_ROWS);      // [RING][128]
-  int* edges = reinterpret_cast<int*>(rows + C::RING * 128);
+  uint32_t* is_tile = rows + C::RING * 128;          // [RING]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   kv4_grid_wait();
   asm volatile("griddepcontrol.launch_dependents;");
@@ -253,6 +247,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
     mbar_init(xch_full, 128);
     mbar_init(xch_empty, 128);
     *abort_word = 0u;
+    *zeroed = 0u;
     fence_barrier_init();
     fence_proxy_async_shared();
   }
@@ -453,7 +448,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
           if (k >= C::RING && !(ok = wait_all(row_empty + at, (k / C::RING - 1) & 1u))) break;
 #pragma unroll
           for (int i = 0; i < 4; ++i) rows[at * 128 + 32 * i + lane] = rw[i];
-          if (lane == 0) edges[at] = w.lim_all - j * 128;
+          if (lane == 0) is_tile[at] = 1u;
           __syncwarp();
           // (testing hook: a tile that is never handed out; the bounded waits on it run out)
           if (lane == 0 && !(k == 0 && static_cast<int>(blockIdx.x) == cp.fault_cta)) mbar_arrive(row_full + at);
@@ -464,7 +459,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         const uint32_t at = k % C::RING;
         if (k >= C::RING) ok = wait_all(row_empty + at, (k / C::RING - 1) & 1u);
         if (lane == 0) {
-          edges[at] = kNoTile;
+          is_tile[at] = 0u;
           mbar_arrive(row_full + at);
         }
       }
@@ -481,17 +476,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
     uint4 kw[NW], vw[NW];
     uint32_t ksf[SfWords<D>::N], vsf_next[SfWords<D>::N], vsf[SfWords<D>::N];
     uint32_t row = kNoRow;                            // cache row of this thread's key in the tile loaded last
-    bool edge = false;                                // some row of the unit does not see the key
     // tile k of the run: its row, K's codes and the scales of both; false: there is none
     auto load_k = [&](uint32_t k) {
       const uint32_t at = k % C::RING;
       if (!(ok = wait_all(row_full + at, (k / C::RING) & 1u))) return false;
-      const int e = edges[at];
+      const bool found = is_tile[at] != 0u;
       row = rows[at * 128 + kr];
-      edge = kr > e;
       __syncwarp();
       if (lane == 0) mbar_arrive(row_empty + at);
-      if (e == kNoTile) return false;
+      if (!found) return false;
 #pragma unroll
       for (int i = 0; i < SfWords<D>::N; ++i) ksf[i] = vsf_next[i] = 0u;
 #pragma unroll
@@ -543,15 +536,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
 #pragma unroll
       for (int i = 0; i < SfWords<D>::N; ++i) vsf[i] = vsf_next[i];
       // A NaN value must reach the rows that see it and no other, and P = 0 would not keep it from a
-      // masked row: where some row does not see the key, its value counts as zero and its key becomes
-      // NaN, so that it arrives through the scores.
-      if (edge) {
-        bool bad = false;
+      // masked row: NaN blocks of values are stored as zeros, and the rows that see them get their NaN
+      // where the segment is written (`zeroed` says that this has happened in the run; the mark is set before
+      // k_full, and so before that segment's last P V).
 #pragma unroll
-        for (int i = 0; i < SfWords<D>::N; ++i) bad = bad || any_nan_scale(vsf[i]);
-        if (bad) {
-#pragma unroll
-          for (int i = 0; i < SfWords<D>::N; ++i) ksf[i] = 0x7F7F7F7Fu, vsf[i] = 0u;
+      for (int i = 0; i < SfWords<D>::N; ++i) {
+        const uint32_t nan = nan_scales(vsf[i]);
+        if (nan != 0u) {
+          vsf[i] &= ~nan;
+          *zeroed = 1u;
         }
       }
       if (k >= 2 && !(ok = wait_all(k_empty + buf, (round - 1) & 1))) break;
@@ -808,6 +801,36 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
               *unit_at(lane, i) = make_uint4(ov[16 * hf + 4 * i], ov[16 * hf + 4 * i + 1], ov[16 * hf + 4 * i + 2],
                                              ov[16 * hf + 4 * i + 3]);
             flush(D * 4, cb * 4 + 64 * hf);
+          }
+        }
+      }
+      // a NaN value was stored as zero: the warp looks at the scales of the segment's values again, and each
+      // row gets its NaN in the blocks of those that it sees
+      if (*zeroed != 0u) {
+        uint32_t nan_blocks = 0u;
+        const unsigned long long bh = w.row / static_cast<unsigned>(R);
+        const int b = static_cast<int>(bh / static_cast<unsigned>(p.c.H));
+        const int h = static_cast<int>(bh % static_cast<unsigned>(p.c.H));
+        const int* table = p.c.block_table + static_cast<long long>(b) * p.c.max_pages;
+        const int behind = min(w.len, w.kt1 * 128);
+        for (int k0 = w.kt0 * 128; k0 < behind; k0 += 32) {
+          const int key = k0 + lane;
+          uint32_t mine = 0u, at;
+          if (key < behind && kv4_row(p.c, table[key >> p.c.page_shift], h, key, at))
+            mine = kv4_nan_blocks<D>(p.c.sf[1], at);
+          for (uint32_t rest = __ballot_sync(0xffffffffu, mine != 0u); rest != 0u; rest &= rest - 1u) {
+            const int s = __ffs(rest) - 1;
+            const uint32_t theirs = __shfl_sync(0xffffffffu, mine, s);
+            if (k0 + s <= lim) nan_blocks |= theirs;
+          }
+        }
+        if (!whole || write) {
+          for (; nan_blocks != 0u; nan_blocks &= nan_blocks - 1u) {
+            const int at = 16 * (__ffs(nan_blocks) - 1);
+            for (int i = 0; i < 16; ++i) {
+              if (whole) reinterpret_cast<uint16_t*>(p.o)[(qrow0 + lane) * D + at + i] = 0x7FFFu;
+              else p.part_o[prow * D + at + i] = __int_as_float(0x7FC00000);
+            }
           }
         }
       }

@@ -96,3 +96,46 @@ def test_maximum_far_along_the_row(cuda_lib, form):
                        new_lens=ints(lens), check=True)
         o, lse = lib.forward_kv4(q, pg.cache, pg.bt, ints(lens), causal=N > 1, check=True)
         check_rows(o, lse, q, pg, lens, N > 1, (0, 1, N // 2, N - 1))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,Hq,roomy", [(1, 4, False), (6, 4, False), (6, 8, False), (20, 8, True), (100, 4, False), (100, 4, True),
+                                        (300, 2, True)])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_nan_goes_where_the_formula_takes_it(cuda_lib, d, N, Hq, roomy, which):
+    """A NaN key: every channel and the LSE of the rows that see it. A NaN value: the 16 channels of its block in the
+    rows that see it, and not the LSE. Everything else is bit for bit what it is without the NaN, wherever the key
+    lies: in front of all queries' positions, among them (some rows see it, some do not), or last."""
+    lib, H, L = cuda_lib, 2, 700
+    per = -(-L // 16)
+    g = torch.Generator().manual_seed(d + N)
+    k, v = (torch.randn((1, H, L, d), generator=g).to(torch.bfloat16) for _ in range(2))
+    q = make_q(1, Hq, N, d, torch.bfloat16, 5)
+    spots = {5, L - N - 1, L - N, L - N // 2 - 1, L - 2, L - 1}
+    for causal in (True, False):
+        for spot in sorted(spots):
+            outs = []
+            for bad in (False, True):
+                pg = Paged(lib, 1, H, d, 16, per, seed=1)
+                if roomy:
+                    pg.bt = torch.cat([pg.bt, torch.full((1, 1 << 14), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
+                lib.kv4_append(pg.cache, k.to(DEV), v.to(DEV), pg.bt, ints([L]), check=True)
+                sf = pg.cache.k_sf if which == "k" else pg.cache.v_sf
+                at = (int(pg.bt[0, spot // 16]), 1, spot % 16)                 # of the second cached head
+                if bad:
+                    sf[at + (1,)] = 0x7F
+                    sf[at + (d // 16 - 1,)] = 0xFF                            # either sign is a NaN
+                outs.append(lib.forward_kv4(q, pg.cache, pg.bt, ints([L]), causal=causal, check=True))
+            (o0, l0), (o1, l1) = outs
+            assert torch.isfinite(o0).all() and torch.isfinite(l0).all()
+            i = torch.arange(N, device=DEV)
+            sees = (L - N + i >= spot) if causal else torch.ones_like(i, dtype=torch.bool)
+            row = torch.zeros((1, Hq, N), dtype=torch.bool, device=DEV)
+            row[:, Hq // 2:] = sees                                            # heads of the second cached head
+            ch = torch.zeros(d, dtype=torch.bool, device=DEV)
+            ch[16:32] = ch[d - 16:] = True
+            want = row[..., None] & (ch if which == "v" else torch.ones_like(ch))
+            assert torch.equal(torch.isnan(o1), want), (causal, spot)
+            assert torch.equal(o1[~want], o0[~want])
+            lost = row if which == "k" else torch.zeros_like(row)
+            assert torch.equal(torch.isnan(l1), lost) and torch.equal(l1[~lost], l0[~lost])
