@@ -16,7 +16,7 @@
  *     code = E2M1 round-to-nearest-even, saturating, of y / s
  *     value read back = code * s * 2^e
  * (quotients in fp32, correctly rounded). E2M1 holds 0, 0.5, 1, 1.5, 2, 3, 4, 6
- * and their negatives: code bit 3 is the sign, bits 0-2 the index in that list.
+ * and their negatives: code bit 3 is the sign (that of x, for zeros too), bits 0-2 the index in that list.
  * An infinite value saturates; a block that holds a NaN gets scale byte 0x7F
  * (NaN) and reads back as NaN.
  *

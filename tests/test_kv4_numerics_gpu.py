@@ -12,7 +12,7 @@ import numpy as np
 import pytest
 import torch
 
-from oracle.kv4 import kv4_attention
+from oracle.kv4 import kv4_attention, kv4_quantize, kv4_rows
 from test_kv4_gpu import DEV, Paged, fill, ints, make_q, n64
 
 pytestmark = pytest.mark.gpu
@@ -139,3 +139,31 @@ def test_nan_goes_where_the_formula_takes_it(cuda_lib, d, N, Hq, roomy, which):
             assert torch.equal(o1[~want], o0[~want])
             lost = row if which == "k" else torch.zeros_like(row)
             assert torch.equal(torch.isnan(l1), lost) and torch.equal(l1[~lost], l0[~lost])
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_keeps_the_sign_of_zeros(cuda_lib, d, dt):
+    """Codes and scale bytes bit for bit where quotients round to zero: zeros of both signs, values far below
+    their block's maximum, on either side of the first border."""
+    g = torch.Generator().manual_seed(d)
+    N = 96
+    x = torch.randn((1, 2, N, d), generator=g)
+    small = torch.exp2(-torch.randint(1, 40, (1, 2, N, d), generator=g).float())
+    x = torch.where(torch.rand((1, 2, N, d), generator=g) < 0.6, x * small, x)
+    x = torch.where(torch.rand((1, 2, N, d), generator=g) < 0.1, torch.copysign(torch.zeros(()), x), x)
+    x[0, 0, 0], x[0, 0, 1], x[0, 1, 0] = 0.0, -0.0, -float(torch.finfo(dt).tiny)
+    x[0, 1, 1, ::2], x[0, 1, 2] = -0.0, -torch.finfo(dt).smallest_normal / 4
+    x = x.to(dt)
+    pg = Paged(cuda_lib, 1, 2, d, 16, N // 16, k_exp=-3, v_exp=2)
+    cuda_lib.kv4_append(pg.cache, x.to(DEV), (-x).to(DEV), pg.bt, ints([N]), check=True)
+    bt = pg.bt[0].cpu().numpy()
+    negative_zeros = 0
+    for sign, codes, sf, e in ((1, pg.cache.k_codes, pg.cache.k_sf, -3), (-1, pg.cache.v_codes, pg.cache.v_sf, 2)):
+        c, s = kv4_quantize(n64(sign * x[0]), e)
+        assert (kv4_rows(sf.cpu().numpy(), bt, 16, 0, N) == s).all()
+        assert (kv4_rows(codes.cpu().numpy(), bt, 16, 0, N) == c).all()
+        negative_zeros += int(((c & 15) == 8).sum() + ((c >> 4) == 8).sum())
+    assert negative_zeros > 1000
+    k, _ = cuda_lib.kv4_read(pg.cache, pg.bt, ints([N]), N, dtype=dt, check=True)
+    assert torch.equal(torch.signbit(k.cpu()), torch.signbit(x))
