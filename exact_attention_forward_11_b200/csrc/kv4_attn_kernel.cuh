@@ -241,10 +241,16 @@ __device__ __forceinline__ void kv4_empty_rows(const Kv4AttnParams& p, int threa
   }
 }
 
+// What a row's unnormalised O is multiplied with. A sum of zero is that of a row without keys (O = 0), or of one
+// whose every score is -infinity (from a query that is infinite: NaN).
+__device__ __forceinline__ float kv4_norm(const Kv4AttnParams& p, float L, bool sees) {
+  return L != 0.f ? f32_exp2i(p.c.exp[1]) / L : sees ? __int_as_float(0x7FC00000) : 0.f;
+}
+
 // One row's result from its unnormalised O (4 channels a lane at d4), maximum and sum.
 template <int D, bool F16>
-__device__ __forceinline__ void kv4_write_row(const Kv4AttnParams& p, size_t row, int d4, float4 a, float M, float L) {
-  const float inv = L == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / L;
+__device__ __forceinline__ void kv4_write_row(const Kv4AttnParams& p, size_t row, int d4, float4 a, float M, float L, bool sees) {
+  const float inv = kv4_norm(p, L, sees);
   reinterpret_cast<uint2*>(p.o)[row * (D / 4) + d4] =
       make_uint2(pack_16<F16>(a.x * inv, a.y * inv), pack_16<F16>(a.z * inv, a.w * inv));
   if (p.lse != nullptr && d4 == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
@@ -676,7 +682,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
     const bool whole = t0 == 0 && t1 == T;
     const int slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
     first_segment = false;
-    const int out_rb = rb, out_n = n;
+    const int out_rb = rb, out_n = n, out_blind = p.causal ? n - len : 0;   // queries before out_blind see no key
     if (tid == 0 && t0 == 0 && !whole) {            // the item's first part: what the join needs
       Kv4Head hd;
       hd.parts = runs.cta_of(item_first + T - 1) - static_cast<int>(blockIdx.x) + 1;
@@ -747,7 +753,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, C::CTAS_PER_SM) kv4_decode_sm1
       if (whole) {
         const int rr = out_rb * ROWS + r;
         if (rr < R && rr % p.N < out_n) {
-          kv4_write_row<D, F16>(p, out_row0 + rr, d4, a, M, L);
+          kv4_write_row<D, F16>(p, out_row0 + rr, d4, a, M, L, rr % p.N >= out_blind);
         }
       } else {
         reinterpret_cast<float4*>(p.part_o)[(static_cast<size_t>(slot) * ROWS + r) * V4 + d4] = a;
@@ -805,7 +811,7 @@ __global__ void __launch_bounds__(256) kv4_join_sm100(const Kv4AttnParams p) {
     }
     M = Mn;
   }
-  const float inv = L == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / L;
+  const float inv = kv4_norm(p, L, L == 0.f && (!p.causal || rr % p.N >= n - kv4_len(p.c, hd.b)));
   const size_t row = (static_cast<size_t>(hd.b) * p.c.H + hd.h) * R + rr;
 #pragma unroll
   for (int e = 0; e < E; ++e)

@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) kv4_chunk_sm100(const Kv4ChunkP
         m_run = M;
       }
       if (whole) {
-        const float inv = l_run == 0.f ? 0.f : f32_exp2i(p.c.exp[1]) / l_run;
+        const float inv = kv4_norm(p, l_run, lim >= 0);
         f0 *= inv;
         f1 *= inv;
       }

@@ -98,7 +98,8 @@ ATTN_API attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block
  *          (must not alias q).
  *   lse  : [B, Hq, N] fp32 (natural log, scale included), or NULL.
  *          Rows i >= q_lens[b] of o and lse are left as they were. A row that sees no
- *          key gets o = 0 and lse = -infinity. A NaN key makes o and lse NaN in the rows
+ *          key gets o = 0 and lse = -infinity; a row whose query holds an infinity or NaN and that
+ *          sees a key gets o = NaN. A NaN key makes o and lse NaN in the rows
  *          that see it, a NaN value the 16 channels of its block in o; all else is unaffected.
  *   workspace : at least attn_fwd_kv4_workspace_bytes(...) bytes, 16-byte aligned,
  *          overwritten; needs no initialisation. Calls that overlap on the GPU, or that

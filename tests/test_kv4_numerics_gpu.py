@@ -21,7 +21,7 @@ pytestmark = pytest.mark.gpu
 FORMS = {"block8": (1, 4), "block16": (4, 4), "one_tile": (20, 4), "two_tiles": (100, 4)}
 
 
-def check_rows(o, lse, q, pg, lens, causal, rows):
+def check_rows(o, lse, q, pg, lens, causal, rows, skip=None):
     eps, tiny = torch.finfo(o.dtype).eps, 2.0 ** -25 if o.dtype == torch.float16 else 0.0
     o64, l64, q64, scale = n64(o), n64(lse), n64(q), 1 / math.sqrt(pg.d)
     worst = 0.0
@@ -31,8 +31,11 @@ def check_rows(o, lse, q, pg, lens, causal, rows):
         ro, rl = kv4_attention(q64[b], k, v, n, causal, scale)
         G = q64.shape[1] // pg.H
         for h in range(q64.shape[1]):
-            for i in [r for r in rows if r < n]:
-                vis = L - n + i + 1 if causal else L
+            for i in [r for r in rows if r < n and not (skip is not None and skip[b, h, r])]:
+                vis = max(0, L - n + i + 1) if causal else L
+                if vis == 0:
+                    assert (o64[b, h, i] == 0).all() and np.isneginf(l64[b, h, i])
+                    continue
                 kk, vv = k[h // G][:vis], v[h // G][:vis]
                 s = scale * kk @ q64[b, h, i]
                 p = np.exp(s - rl[h, i])
@@ -167,3 +170,31 @@ def test_append_keeps_the_sign_of_zeros(cuda_lib, d, dt):
     assert negative_zeros > 1000
     k, _ = cuda_lib.kv4_read(pg.cache, pg.bt, ints([N]), N, dtype=dt, check=True)
     assert torch.equal(torch.signbit(k.cpu()), torch.signbit(x))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("what", [float("inf"), float("-inf"), float("nan")])
+def test_infinite_and_nan_queries(cuda_lib, form, what):
+    """A query row that holds an infinity or NaN has no finite softmax: its O is NaN where it sees a key (whatever the
+    signs of the keys it meets), zero where it sees none, and the other rows are right. (Not bit for bit what they
+    are beside a finite row: rows of a block move the value they subtract together.)"""
+    lib, d, (N, Hq) = cuda_lib, 128, FORMS[form]
+    for L, causal in ((40, True), (40, False), (1, True), (700, True)):
+        pg = Paged(lib, 1, 1, d, 16, 44, seed=2)
+        if form == "one_tile":
+            pg.bt = torch.cat([pg.bt, torch.full((1, 1 << 14), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
+        g = torch.Generator().manual_seed(L)
+        k, v = (torch.randn((1, 1, L, d), generator=g) for _ in range(2))
+        k[..., 7] = k[..., 7].abs() + 1.0                                   # one channel of one sign, and not zero
+        lib.kv4_append(pg.cache, k.to(torch.bfloat16).to(DEV), v.to(torch.bfloat16).to(DEV), pg.bt, ints([L]), check=True)
+        q = make_q(1, Hq, N, d, torch.bfloat16, 3)
+        bad = torch.zeros((1, Hq, N), dtype=torch.bool, device=DEV)
+        bad[0, 1, N - 1] = bad[0, Hq - 1, 0] = bad[0, 0, N // 2] = True
+        for channel in (7, 50):                                            # scores all of one sign, and of both
+            qb = q.clone()
+            qb[..., channel] = torch.where(bad, what, q[..., channel])
+            o1, l1 = lib.forward_kv4(qb, pg.cache, pg.bt, ints([L]), causal=causal, check=True)
+            sees = (L - N + torch.arange(N, device=DEV) >= 0) | (not causal)
+            lost = bad & sees
+            assert torch.equal(torch.isnan(o1), lost[..., None].expand_as(o1)), (L, causal, channel)
+            check_rows(o1, l1, q, pg, [L], causal, sorted({0, 1, N // 2, N - 1}), skip=lost)
