@@ -501,8 +501,9 @@ def backward(q, k, v, o, lse, dout, causal=False, scale=None, dq=None, dk=None, 
 
 
 # split-K workspaces of w4a16_matmul, one per (device, stream): zeroed when
-# allocated; every call leaves the tickets zero again
+# allocated; every call leaves the tickets, its first bytes, zero again
 _W4_WORKSPACES = {}
+_W4_TICKET_BYTES = 4864
 
 
 def _reset_w4_workspaces():
@@ -515,8 +516,17 @@ def _reset_w4_workspaces():
     torch.cuda.synchronize()
 
 
-def _w4_workspace(device, stream_ptr, nbytes):
+def _w4_workspace(device, stream, stream_ptr, nbytes):
     import torch
+    if stream is not None or torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device), torch.cuda.stream(stream):  # (a stream of None changes nothing)
+            return _w4_workspace(device, None, stream_ptr, nbytes)
+    if torch.cuda.is_current_stream_capturing():
+        # a graph has its own, zeroed in every replay: it may be replayed on any stream, next to any other
+        # call, and after the cached one has been replaced by a larger one
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws[:_W4_TICKET_BYTES].zero_()
+        return ws
     key = (device.index, stream_ptr)
     ws = _W4_WORKSPACES.get(key)
     if ws is None or ws.numel() < nbytes:
@@ -535,7 +545,7 @@ def w4a16_matmul(x, qweight, scales, zeros, out=None, stream=None, check=False, 
     split_k=True (default) runs w4a16_gemm_splitk, which balances the K slices over
     every SM; its workspace is `workspace` (a zeroed uint8 CUDA tensor of at least
     w4a16_gemm_splitk_workspace_bytes(M, N, K) bytes) or one cached per device and
-    stream. split_k=False runs w4a16_gemm (one CTA per 128 output columns)."""
+    stream (inside a graph capture: the graph's own). split_k=False runs w4a16_gemm (one CTA per 128 output columns)."""
     import torch
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
@@ -558,7 +568,7 @@ def w4a16_matmul(x, qweight, scales, zeros, out=None, stream=None, check=False, 
     if need == 0:
         raise AttnError(ATTN_ERR_UNSUPPORTED, "w4a16_gemm_splitk_workspace_bytes")
     if workspace is None:
-        workspace = _w4_workspace(x.device, sp, need)
+        workspace = _w4_workspace(x.device, stream, sp, need)
     elif workspace.device != x.device or not workspace.is_contiguous() or \
             workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {x.device}")

@@ -85,3 +85,74 @@ def test_layer_of_projections_of_different_widths(cuda_lib):
         for p, y in zip(layer, ys):
             p.check(y)
     assert lib.attn_get_device_status(None) == lib.ATTN_OK
+
+
+@pytest.mark.gpu
+def test_captured_products_have_workspaces_of_their_own(cuda_lib):
+    """Graphs captured on a stream whose cached workspace exists: replayed on two streams at once, between eager
+    calls on the capture stream, and after a larger product has replaced the cached workspace."""
+    lib = cuda_lib
+    small, wide, big = Product(8, 4096, 1024, 1), Product(16, 2048, 6144, 2), Product(128, 4096, 8192, 3)
+    side, streams = torch.cuda.Stream(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        want = [lib.w4a16_matmul(p.x, *p.w, check=True) for p in (small, wide)]
+    for p, y in zip((small, wide), want):
+        p.check(y)
+    graphs, outs = [], []
+    for p in (small, wide):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            first = lib.w4a16_matmul(p.x, *p.w)
+            second = lib.w4a16_matmul(small.x, *small.w)
+        graphs.append(g)
+        outs.append((first, second))
+    cached = lib._W4_WORKSPACES[(0, side.cuda_stream)]
+    before = cached.data_ptr()
+    for round_ in range(4):
+        for pair in outs:
+            for y in pair:
+                y.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for s, g in zip(streams, graphs):
+                with torch.cuda.stream(s):
+                    g.replay()
+            with torch.cuda.stream(side):
+                eager = lib.w4a16_matmul(wide.x, *wide.w)
+        torch.cuda.synchronize()
+        assert torch.equal(eager, want[1])
+        for (first, second), w in zip(outs, want):
+            assert torch.equal(first, w) and torch.equal(second, want[0])
+        if round_ == 1:                                                    # a larger one replaces the cached workspace
+            big.check(lib.w4a16_matmul(big.x, *big.w, stream=side, check=True))
+            assert lib._W4_WORKSPACES[(0, side.cuda_stream)].data_ptr() != before
+            del cached
+            torch.cuda.empty_cache()
+    assert lib.attn_get_device_status(None) == lib.ATTN_OK
+
+
+@pytest.mark.gpu
+def test_capture_without_an_eager_call_first(cuda_lib):
+    """On a stream that has no cached workspace yet, with a fork to a second stream inside the capture."""
+    lib = cuda_lib
+    a, b = Product(4, 2048, 4096, 5), Product(16, 2048, 6144, 6)
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        ya = lib.w4a16_matmul(a.x, *a.w)
+        yb = torch.empty((16, 6144), dtype=torch.float16, device=DEV)
+        lib.w4a16_matmul(b.x, *b.w, out=yb, stream=side)
+        main.wait_stream(side)
+        yc = lib.w4a16_matmul(b.x, *b.w)
+    for _ in range(3):
+        for y in (ya, yb, yc):
+            y.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        a.check(ya)
+        b.check(yb)
+        assert torch.equal(yb, yc)
+    assert lib.attn_get_device_status(None) == lib.ATTN_OK
