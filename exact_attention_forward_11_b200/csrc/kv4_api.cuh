@@ -7,6 +7,12 @@ namespace {
 // the int32 arrays may be slices of larger ones
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// whether two arrays of `bytes` bytes share any
+bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return (x < y ? y - x : x - y) < bytes;
+}
+
 attn_status kv4_check_cache(const attn_kv4_cache* c, const int* block_table, const int* seq_lens, int B, int N,
                             int max_pages, int dtype) {
   if (c == nullptr || c->k_codes == nullptr || c->k_sf == nullptr || c->v_codes == nullptr || c->v_sf == nullptr ||
@@ -178,6 +184,7 @@ attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block_table, c
   if (k == nullptr || v == nullptr) return ATTN_ERR_INVALID_ARG;
   if (attn_status s = kv4_check_cache(cache, block_table, seq_lens, B, N, max_pages, dtype); s != ATTN_OK) return s;
   if (!aligned16(k) || !aligned16(v) || !aligned4(starts)) return ATTN_ERR_MISALIGNED;
+  if (overlap(k, v, static_cast<size_t>(B) * cache->Hkv * N * cache->d * 2)) return ATTN_ERR_INVALID_ARG;
   attn::Kv4MoveParams p{};
   p.c = kv4_cache_of(cache, block_table, seq_lens, B, max_pages);
   p.out[0] = static_cast<uint8_t*>(k);
@@ -219,6 +226,7 @@ attn_status fwd_kv4(const attn_kv4_cache* cache, const void* q, const int* block
   if (!plan.fits || workspace == nullptr || workspace_bytes < plan.workspace) return ATTN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned4(q_lens) || !aligned16(workspace))
     return ATTN_ERR_MISALIGNED;
+  if (overlap(q, o, static_cast<size_t>(B) * Hq * N * d * 2)) return ATTN_ERR_INVALID_ARG;
   attn::Kv4AttnParams p{};
   p.c = kv4_cache_of(cache, block_table, seq_lens, B, max_pages);
   p.q = static_cast<const uint8_t*>(q);

@@ -78,9 +78,9 @@ ATTN_API attn_status attn_kv4_append(const attn_kv4_cache* cache, const void* k,
 
 /*
  * attn_kv4_read - reads positions back.
- *   k, v   : [B, Hkv, N, d] outputs: row i holds position starts[b] + i, rounded once
- *            to dtype (exact where the format holds it: 6 significant bits); rows at
- *            or behind seq_lens[b] are written as zeros.
+ *   k, v   : [B, Hkv, N, d] outputs that do not overlap (else ATTN_ERR_INVALID_ARG): row
+ *            i holds position starts[b] + i, rounded once to dtype (exact where the format
+ *            holds it: 6 significant bits); rows at or behind seq_lens[b] are written as zeros.
  *   starts : [B] int32, 0 or more, or NULL for 0.
  */
 ATTN_API attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block_table, const int* seq_lens,
@@ -95,7 +95,7 @@ ATTN_API attn_status attn_kv4_read(const attn_kv4_cache* cache, const int* block
  *          token at position seq_lens[b] - q_lens[b] + i; it sees the keys at positions
  *          j < seq_lens[b], and with causal = 1 only j <= its own.
  *   o    : [B, Hq, N, d] output softmax(scale q K^T) V over the values as read back
- *          (must not alias q).
+ *          (must not overlap q: ATTN_ERR_INVALID_ARG).
  *   lse  : [B, Hq, N] fp32 (natural log, scale included), or NULL.
  *          Rows i >= q_lens[b] of o and lse are left as they were. A row that sees no
  *          key gets o = 0 and lse = -infinity; a row whose query holds an infinity or NaN and that

@@ -146,3 +146,15 @@ def test_handle_is_fixed_and_streams_of_another_device_are_refused(cuda_lib):
     with pytest.raises(ValueError):
         lib.kv4_read(c, bt, sl, 4, stream=Elsewhere())
     torch.cuda.synchronize()
+
+
+def test_overlapping_arrays_are_refused(lib):
+    """Outputs that overlap one another, or the queries, would be written by CTAs in no order."""
+    row = 2 * 3 * 128 * 2                                          # bytes of k: [1, 2, 3, 128]
+    for v in (FAKE, FAKE + 16, FAKE - 16, FAKE + row - 16, FAKE - row + 16):
+        addr, a = split(MOVE, dict(v=v))
+        assert lib.attn_kv4_read(addr, a["bt"], a["sl"], a["first"], a["k"], a["v"], a["B"], a["N"], a["maxp"], a["dtype"],
+                                 a["stream"]) == 1
+    for o in (FAKE, FAKE + 16, FAKE - 2 * row + 16, FAKE + 2 * row - 16):    # q: [1, 4, 3, 128]
+        addr, a = split(FWD, dict(o=o))
+        assert lib.attn_fwd_kv4(addr, *a.values()) == 1
