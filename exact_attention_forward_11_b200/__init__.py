@@ -603,6 +603,8 @@ class KV4Cache:
             _expect(t, name, (P, H, S, width), torch.uint8, k_codes.device)
         struct = attn_kv4_cache(*(t.data_ptr() for t in (k_codes, k_sf, v_codes, v_sf)), P, S, H, 2 * half,
                                 operator.index(k_exp), operator.index(v_exp))
+        if (struct.k_exp, struct.v_exp) != (k_exp, v_exp):      # a C int would wrap
+            raise ValueError("k_exp and v_exp must lie in [-32, 32]")
         for name, value in dict(k_codes=k_codes, k_sf=k_sf, v_codes=v_codes, v_sf=v_sf, k_exp=struct.k_exp,
                                 v_exp=struct.v_exp, num_pages=P, heads=H, page_size=S, d=2 * half,
                                 device=k_codes.device, _index=k_codes.get_device(), _struct=struct,

@@ -158,3 +158,13 @@ def test_overlapping_arrays_are_refused(lib):
     for o in (FAKE, FAKE + 16, FAKE - 2 * row + 16, FAKE + 2 * row - 16):    # q: [1, 4, 3, 128]
         addr, a = split(FWD, dict(o=o))
         assert lib.attn_fwd_kv4(addr, *a.values()) == 1
+
+
+@pytest.mark.parametrize("exps", [((1 << 32) + 1, 0), (0, -(1 << 32)), (1 << 31, 0)])
+def test_exponents_that_a_c_int_would_wrap(monkeypatch, exps):
+    monkeypatch.setattr(attn, "_expect", lambda *a: None)          # (host tensors stand in for the cache's)
+    u = lambda *s: torch.zeros(s, dtype=torch.uint8)                                # noqa: E731
+    tensors = u(4, 2, 16, 64), u(4, 2, 16, 8), u(4, 2, 16, 64), u(4, 2, 16, 8)
+    assert attn.KV4Cache(*tensors, k_exp=-3, v_exp=32).k_exp == -3
+    with pytest.raises(ValueError):
+        attn.KV4Cache(*tensors, *exps)
