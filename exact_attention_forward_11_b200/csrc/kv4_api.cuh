@@ -61,14 +61,20 @@ struct Kv4Plan {
 constexpr int kKv4Sms = 148;
 // The kernel, by the rows of a cached head and the work: the decode kernel in blocks of 8 (nt = 1) or 16 rows (2; a
 // block reads the keys again, from L2), or the chunk kernel (0). Work is the units of Kv4Runs at the table's full
-// length, an item counting as its tiles and two. Both sides measured (d = 128, 8 cached heads unless said):
-//   * 9 to 16 and 25 to 32 rows: blocks of 16 (16 sequences of 4000 keys, 16 rows 33.0 us, in blocks of 8 38.4; 32
+// length (the host does not know the sequences': a table with room counts as full), an item counting as its tiles and
+// two. Both sides measured (8 cached heads unless said, d = 128 / d = 64, us):
+//   * 9 to 16 and 25 to 32 rows: blocks of 16 (16 sequences of 4000 keys, d = 128: 16 rows 33.0, in blocks of 8 38.4; 32
 //     rows 60 and 69). 17 to 24 rows: three blocks of 8 instead of two of 16 (54.7 and 59.1).
-//   * above 32 rows: the chunk kernel (32 sequences of 8192 keys, 40 rows 219 us and 258; 8 of 6000 keys, 64 rows 60.6 and
-//     76), but the decode kernel for up to 1024 units of 16 rows, where its start is the shorter (6 of 1000 keys, 48 rows:
-//     864 units, 13.5 us and 27.3; 960 units 17.6 and 20.4; 1152 units 22.0 and 24.4, 1536 units 23.0 and 22.8).
-//   * blocks of 8 for any rows up to 512 units of 8 rows (512 units: 8.4 us and 10.4; 768: 14.5 and 13.2).
-constexpr int kKv4DecodeRows = 32, kKv4DecodeUnits = 1024, kKv4SmallUnits = 512;
+//   * above 32 rows: the chunk kernel (d = 128: 32 sequences of 8192 keys, 40 rows 219 and in the decode kernel 258; 8 of
+//     6000 keys, 64 rows 60.6 and 76), but the decode kernel for up to 1600 units of 16 rows, where its start is the
+//     shorter. Decode against chunk kernel: 864 units (48 rows, 6 x 1000 keys) 13.7 and 28.1 / 11.2 and 22.0; 1120 (100
+//     rows, 2 x 2000) 18.5 and 28.1 / 15.3 and 21.4; 1536 (40 rows, 16 x 300) 22.7 and 27.0 / 18.0 and 21.2; 1680 (100 rows,
+//     3 x 2000) 28.5 and 27.9 / 22.6 and 21.9; 1728 (48 rows, 12 x 1000) 25.0 and 34.9 / 18.3 and 26.6; 1920 (40 rows,
+//     20 x 300) 29.1 and 28.8 / 22.8 and 22.4; 2240 (100 rows, 4 x 2000) 35.0 and 30.4 / 27.2 and 23.4.
+//   * blocks of 8 for any rows up to 512 units of 8 rows. Blocks of 8 against 16: 320 units (32 rows, 2 x 700 keys) 9.4 and
+//     11.3 / 8.1 and 9.3; 512 (64 rows, 2 x 500) 8.6 and 10.6 / 7.5 and 8.8; 640 (32 rows, 4 x 700) 12.2 and 11.5 / 9.6 and
+//     9.7; 768 (16 rows, 8 x 1000) 14.4 and 13.4 / 11.1 and 10.9.
+constexpr int kKv4DecodeRows = 32, kKv4DecodeUnits = 1600, kKv4SmallUnits = 512;
 
 Kv4Plan kv4_plan(int B, int Hq, int Hkv, int N, int d, int page_size, int max_pages) {
   Kv4Plan r;

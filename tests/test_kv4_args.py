@@ -168,3 +168,20 @@ def test_exponents_that_a_c_int_would_wrap(monkeypatch, exps):
     assert attn.KV4Cache(*tensors, k_exp=-3, v_exp=32).k_exp == -3
     with pytest.raises(ValueError):
         attn.KV4Cache(*tensors, *exps)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_kernel_of_short_chunks(lib, d):
+    """Above 32 rows the decode kernel runs up to 1600 units of 16 rows (both kernels are measured around it in
+    csrc/kv4_api.cuh): its workspace has blocks of 16 rows, the chunk kernel's of 256."""
+    def blocks_of_16(B, N, keys):                                  # 32 query heads on 8
+        pages = -(-keys // 16)
+        rows, tiles = 4 * N, -(-pages * 16 // 256)
+        assert rows > 32
+        small = lib.attn_fwd_kv4_workspace_bytes(B, 32, 8, N, d, 16, pages) < 2 * 148 * 17 * (4 * d + 8)
+        return small, (tiles + 2) * B * 8 * -(-rows // 16)
+    assert blocks_of_16(6, 12, 1000) == (True, 864)
+    assert blocks_of_16(9, 12, 1000) == (True, 1296)
+    assert blocks_of_16(16, 10, 300) == (True, 1536)
+    assert blocks_of_16(3, 25, 2000) == (False, 1680)
+    assert blocks_of_16(4, 25, 2000) == (False, 2240)
