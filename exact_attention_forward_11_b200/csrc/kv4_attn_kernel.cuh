@@ -37,13 +37,14 @@
 // segment's way, 18.4 against 14.4 us on 6 sequences of up to 2047 keys x 12 heads.)
 //
 // Bound: HBM at 4.5 bits a value is 12e12 values / s, 41 per SM and clock; a value costs half a
-// conversion and half a multiplication (64 lanes / clk / SM each), and with everything else 2.3
+// conversion and half a multiplication (64 lanes / clk / SM each), and with everything else 2.2
 // instructions of a lane. Measured (32 sequences of 32768 keys x 8 heads, d = 128, one token, 4 query heads to a key
-// head): 218 us, 5.5 TB/s of the cache's bytes, 0.84 of the measured copy rate, at 64 % of the issue slots;
-// after a second under the power cap (1.77 instead of 1.965 GHz) 252 us. The list of a run starts after about 7 us
-// (lengths, page numbers, first codes: a chain of three memory latencies) and each further segment costs
-// about 2 us, which is what small batches spend their time on (16 sequences of up to 4096 keys: 23.0 us
-// for 8.1 us of bytes).
+// head): 220 us, 5.5 TB/s of the cache's bytes, 0.84 of the measured copy rate, at 62 % of the issue slots;
+// after a second under the power cap (1.77 instead of 1.965 GHz) 260 us. Small batches spend their time around the
+// steps. Clock stamps, us after the wait for the kernel before, inputs out of L2: one sequence of 509 keys: lengths read
+// 0.7, segment found 1.8, first copies issued 2.7, q ready 3.6, first stage there 3.7, its one step done 5.7, written 7.0,
+// next kernel past its wait 7.9; 16 sequences of up to 4096 keys (mean of 296 CTAs): 1.0, 2.1, 4.5, 6.4, 6.5, and the CTAs
+// end between 16 and 20; the join's wait ends 1.0 later and the join itself takes 3.4 (23.0 us a call for 8.1 us of bytes).
 #pragma once
 
 #include "kv4_cache_kernel.cuh"

@@ -30,10 +30,11 @@
 // keys); 14-15 write the rows that see no key. TMEM and MMA order: attn_fwd_kernel.cuh.
 // Bound: 4 * 128 * 128 * D operations of a (tile, 128 keys) take 1024 clocks of the tensor pipe at
 // D = 128, its 16384 exponentials 1024 clocks of the MUFU units. Measured: 2048 queries x 32 heads (8 cached)
-// over 32768 keys, causal: 1.05 ms, 1010 TFLOP/s, 0.60 of the measured bf16 burst rate (0.72 of the sustained; without
+// over 32768 keys, causal: 1.06 ms, 1000 TFLOP/s, 0.60 of the measured bf16 burst rate (0.71 of the sustained; without
 // the conversion, which is then wrong, 0.96 ms); a step of two row tiles takes 2.3 us, of which a
 // softmax group works 1.5 and waits for its next S the rest. A run starts after 9 us and a further
-// segment costs about 6 us: 4 sequences of 238 to 512 queries x 28 heads over 2109 to 4096 keys take 131 us (510 TFLOP/s).
+// segment costs about 6 us: 4 sequences of 238 to 512 queries x 28 heads over 2109 to 4096 keys take 131 to 141 us (470 to
+// 510 TFLOP/s).
 #pragma once
 
 #include "attn_fwd_kernel.cuh"
